@@ -7,6 +7,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -30,7 +31,8 @@ SYMBOLS = ("tq_quantize_append", "tq_decode_workspace_bytes", "tq_decode_chunk_t
            "tq_decode_append_host_srft_workspace_bytes", "tq_sdpa_int4_decode_append_srft_host",
            "tq_decode_append_host_cb_workspace_bytes", "tq_sdpa_cb_decode_append_host",
            "tq_uniform_levels", "tq_quantize_append_uniform", "tq_sdpa_uniform_decode_append",
-           "tq_sdpa_uniform_decode_append_host", "tq_status_string")
+           "tq_sdpa_uniform_decode_append_host", "tq_quantize_append_q8", "tq_read_q8",
+           "tq_sdpa_q8_workspace_bytes", "tq_sdpa_q8", "tq_sdpa_q8_decode_append", "tq_status_string")
 
 _lib = None
 
@@ -126,6 +128,19 @@ def load() -> ctypes.CDLL:
     lib.tq_sdpa_uniform_decode_append.restype = i32
     lib.tq_sdpa_uniform_decode_append_host.argtypes = lib.tq_sdpa_cb_decode_append_host.argtypes
     lib.tq_sdpa_uniform_decode_append_host.restype = i32
+    lib.tq_quantize_append_q8.argtypes = [P, P, i32, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P,
+                                          i64, P]
+    lib.tq_quantize_append_q8.restype = i32
+    lib.tq_read_q8.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, i32, P, P, i32, P, P, i32, P]
+    lib.tq_read_q8.restype = i32
+    lib.tq_sdpa_q8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.tq_sdpa_q8_workspace_bytes.restype = sz
+    lib.tq_sdpa_q8.argtypes = [P, i32, i32, i32, i32, i32, i32, i32, i32, P, P, P, P, i64, P, P, i32,
+                               f32, P, i32, P, P, sz, P]
+    lib.tq_sdpa_q8.restype = i32
+    lib.tq_sdpa_q8_decode_append.argtypes = [P, i32, P, P, i32, i32, i32, i32, i32, i32, i32, P, P, P,
+                                             P, i64, P, i32, f32, P, i32, P, P, sz, P]
+    lib.tq_sdpa_q8_decode_append.restype = i32
     lib.tq_status_string.argtypes = [i32]
     lib.tq_status_string.restype = ctypes.c_char_p
     lib.tq_set_test_hooks.argtypes = [ctypes.c_uint32]
@@ -616,3 +631,218 @@ def bind_sdpa_cb_decode_append_host(q_host, k_new_host, v_new_host, k_packed, k_
             levels, out_host, workspace)
     name = "tq_sdpa_uniform_decode_append_host" if uniform else "tq_sdpa_cb_decode_append_host"
     return BoundCall(getattr(load(), name), args, name, keep)
+
+
+# ------------------------------------------------- the 8-bit block-scaled cache
+
+TQ_Q8_INT8, TQ_Q8_E4M3 = 0, 1
+_Q8_FORMATS = {torch.int8: TQ_Q8_INT8, torch.float8_e4m3fn: TQ_Q8_E4M3}
+_DTYPES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16}
+
+
+def _dtype_of(dtype: torch.dtype) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"expected float32 or bfloat16, got {dtype}")
+    return code
+
+
+def _q8_check(k_codes, k_scales, v_codes, v_scales, block, *others):
+    """The checks every q8 call makes of its tensors; returns (device index, B, Hkv,
+    capacity, d, format code)."""
+    device = k_codes.device
+    if device.type != "cuda":
+        raise ValueError("all tensors must be contiguous CUDA tensors")
+    for t in (k_codes, k_scales, v_codes, v_scales, *others):
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+    fmt = _Q8_FORMATS.get(k_codes.dtype)
+    if fmt is None or v_codes.dtype != k_codes.dtype:
+        raise TypeError("codes must be int8 or float8_e4m3fn, the same for K and V")
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32:
+        raise TypeError("scales must be float32")
+    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+        raise ValueError("codes must be [B][Hkv][capacity][d], the same for K and V")
+    B, H, cap, d = k_codes.shape
+    if block < 1 or k_scales.shape != (B, H, -(-cap // block)) or v_scales.shape != k_scales.shape:
+        raise ValueError("scales must be [B][Hkv][ceil(capacity / block)]")
+    return device, B, H, cap, d, fmt
+
+
+def _q8_lens(B, **lens):
+    for name, t in lens.items():
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != B):
+            raise ValueError(f"{name} must be int32 [B]")
+
+
+class _Launch:
+    """The device and stream a q8 call runs on: the tensors' device, and there the
+    given stream or the current one.  Buffers a call allocates belong to that stream."""
+
+    __slots__ = ("device", "stream", "_ctx")
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        if self.stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self._ctx = None
+        if stream is not None or device.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def quantize_append_q8(k, v, pos, k_codes, k_scales, v_codes, v_scales, block, n_valid=None,
+                       stream=None):
+    """Quantize k, v [B][Hkv][n][d] into rows pos[b] .. pos[b]+n-1 of an 8-bit block-scaled
+    cache (codes [B][Hkv][capacity][d] int8 or float8_e4m3fn, scales [B][Hkv][blocks]); of
+    sequence b only the first n_valid[b] tokens, where n_valid is given."""
+    device, B, H, cap, d, fmt = _q8_check(k_codes, k_scales, v_codes, v_scales, block, k, v, pos, n_valid)
+    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B or k.shape[1] != H or k.shape[3] != d:
+        raise ValueError("k and v must be [B][Hkv][n][d]")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must share dtype")
+    _q8_lens(B, pos=pos, n_valid=n_valid)
+    with _Launch(device, stream) as s:
+        rc = load().tq_quantize_append_q8(k.data_ptr(), v.data_ptr(), _dtype_of(k.dtype), B, H, k.shape[2],
+                                          d, fmt, block, pos.data_ptr(), _ptr(n_valid), k_codes.data_ptr(),
+                                          k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                                          cap, s)
+    if rc != TQ_OK:
+        raise TQError(rc, "tq_quantize_append_q8")
+
+
+def read_q8(k_codes, k_scales, v_codes, v_scales, block, pos, rows, n_valid=None,
+            dtype=torch.bfloat16, out=None, stream=None):
+    """The values (k, v) [B][Hkv][rows][d] of cache rows pos[b] .. pos[b]+rows-1 (pos None:
+    from row 0) in dtype.  Rows outside the cache, or at n_valid[b] and behind, are left as
+    they are in out = (k_out, v_out); without out they are zeros."""
+    ko, vo = (None, None) if out is None else out
+    device, B, H, cap, d, fmt = _q8_check(k_codes, k_scales, v_codes, v_scales, block, pos, n_valid, ko, vo)
+    _q8_lens(B, pos=pos, n_valid=n_valid)
+    with _Launch(device, stream) as s:
+        if out is None:
+            # without pos and n_valid every row inside the cache is written
+            whole = pos is None and n_valid is None and rows <= cap
+            make = torch.empty if whole else torch.zeros
+            ko = make(B, H, rows, d, dtype=dtype, device=device)
+            vo = make(B, H, rows, d, dtype=dtype, device=device)
+        elif ko.shape != (B, H, rows, d) or vo.shape != ko.shape or ko.dtype != vo.dtype:
+            raise ValueError("out must be two tensors [B][Hkv][rows][d] of one dtype")
+        rc = load().tq_read_q8(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                               v_scales.data_ptr(), cap, B, H, d, fmt, block, _ptr(pos), _ptr(n_valid),
+                               rows, ko.data_ptr(), vo.data_ptr(), _dtype_of(ko.dtype), s)
+    if rc != TQ_OK:
+        raise TQError(rc, "tq_read_q8")
+    return ko, vo
+
+
+def sdpa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx,
+                            dtype=torch.float32) -> int:
+    return int(load().tq_sdpa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx,
+                                                 _dtype_of(dtype)))
+
+
+def _q8_workspace(workspace, B, Hq, H, d, n, max_ctx, out_code, device):
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    need = load().tq_sdpa_q8_workspace_bytes(B, Hq, H, d, n, max_ctx, out_code)
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=device), need
+
+
+def _q8_out(out, lse, shape, dtype, device, make):
+    if out is None:
+        out = make(shape, dtype=dtype, device=device)
+    elif out.shape != shape:
+        raise ValueError("out must have the shape of q")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (*shape[:-1], 2)):
+        raise ValueError("lse must be float32, the shape of q with 2 in the place of d")
+    return out
+
+
+def sdpa_q8(q, k_codes, k_scales, v_codes, v_scales, block, ctx_lens, max_ctx, q_lens=None,
+            attn_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of each sequence's newest tokens over its 8-bit block-scaled cache: query i
+    of q [B][Hq][n][d] sits at position ctx_lens[b] - q_lens[b] + i (q_lens None: n for
+    every sequence; their own rows are in the cache already) and attends the rows up to it.
+    Returns out [B][Hq][n][d], by default of q's dtype; queries at q_lens[b] and behind are
+    left as they are in out, or zeros where it is allocated here."""
+    device, B, H, cap, d, fmt = _q8_check(k_codes, k_scales, v_codes, v_scales, block, q, ctx_lens, q_lens,
+                                          out, lse, workspace)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
+        raise ValueError("q must be [B][Hq][n][d]")
+    _q8_lens(B, ctx_lens=ctx_lens, q_lens=q_lens)
+    Hq, n = q.shape[1], q.shape[2]
+    with _Launch(device, stream) as s:
+        out = _q8_out(out, lse, q.shape, q.dtype, device, torch.empty if q_lens is None else torch.zeros)
+        code = _dtype_of(out.dtype)
+        workspace, ws_bytes = _q8_workspace(workspace, B, Hq, H, d, n, max_ctx, code, device)
+        rc = load().tq_sdpa_q8(q.data_ptr(), _dtype_of(q.dtype), B, Hq, H, n, d, fmt, block,
+                               k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                               v_scales.data_ptr(), cap, ctx_lens.data_ptr(), _ptr(q_lens), max_ctx,
+                               1.0 / math.sqrt(d) if attn_scale is None else attn_scale, out.data_ptr(),
+                               code, _ptr(lse), workspace.data_ptr(), ws_bytes, s)
+    if rc != TQ_OK:
+        raise TQError(rc, "tq_sdpa_q8")
+    return out
+
+
+def sdpa_q8_decode(q, k_codes, k_scales, v_codes, v_scales, block, ctx_lens, max_ctx,
+                   attn_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Decode over an 8-bit block-scaled cache: q [B][Hq][d] attends rows
+    0 .. ctx_lens[b]-1; returns out [B][Hq][d], fp32 unless out is given."""
+    device, B, H, cap, d, fmt = _q8_check(k_codes, k_scales, v_codes, v_scales, block, q, ctx_lens, out, lse,
+                                          workspace)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+        raise ValueError("q must be [B][Hq][d]")
+    _q8_lens(B, ctx_lens=ctx_lens)
+    Hq = q.shape[1]
+    with _Launch(device, stream) as s:
+        out = _q8_out(out, lse, q.shape, torch.float32, device, torch.empty)
+        code = _dtype_of(out.dtype)
+        workspace, ws_bytes = _q8_workspace(workspace, B, Hq, H, d, 1, max_ctx, code, device)
+        rc = load().tq_sdpa_q8(q.data_ptr(), _dtype_of(q.dtype), B, Hq, H, 1, d, fmt, block,
+                               k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                               v_scales.data_ptr(), cap, ctx_lens.data_ptr(), None, max_ctx,
+                               1.0 / math.sqrt(d) if attn_scale is None else attn_scale, out.data_ptr(),
+                               code, _ptr(lse), workspace.data_ptr(), ws_bytes, s)
+    if rc != TQ_OK:
+        raise TQError(rc, "tq_sdpa_q8")
+    return out
+
+
+def sdpa_q8_decode_append(q, k_new, v_new, k_codes, k_scales, v_codes, v_scales, block, ctx_lens,
+                          max_ctx, attn_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """One decode step: quantize k_new, v_new [B][Hkv][1][d] into row ctx_lens[b]-1, then
+    sdpa_q8_decode over rows 0 .. ctx_lens[b]-1 (lengths include the new token)."""
+    device, B, H, cap, d, fmt = _q8_check(k_codes, k_scales, v_codes, v_scales, block, q, k_new, v_new,
+                                          ctx_lens, out, lse, workspace)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+        raise ValueError("q must be [B][Hq][d]")
+    if k_new.shape != (B, H, 1, d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [B][Hkv][1][d]")
+    if k_new.dtype != v_new.dtype:
+        raise TypeError("k_new and v_new must share dtype")
+    _q8_lens(B, ctx_lens=ctx_lens)
+    Hq = q.shape[1]
+    with _Launch(device, stream) as s:
+        out = _q8_out(out, lse, q.shape, torch.float32, device, torch.empty)
+        code = _dtype_of(out.dtype)
+        workspace, ws_bytes = _q8_workspace(workspace, B, Hq, H, d, 1, max_ctx, code, device)
+        rc = load().tq_sdpa_q8_decode_append(
+            q.data_ptr(), _dtype_of(q.dtype), k_new.data_ptr(), v_new.data_ptr(), _dtype_of(k_new.dtype),
+            B, Hq, H, d, fmt, block, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+            v_scales.data_ptr(), cap, ctx_lens.data_ptr(), max_ctx,
+            1.0 / math.sqrt(d) if attn_scale is None else attn_scale, out.data_ptr(), code, _ptr(lse),
+            workspace.data_ptr(), ws_bytes, s)
+    if rc != TQ_OK:
+        raise TQError(rc, "tq_sdpa_q8_decode_append")
+    return out

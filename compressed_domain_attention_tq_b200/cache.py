@@ -332,3 +332,88 @@ class UniformKVCache(CodebookKVCache):
                                                         self.bits, self.levels, attn_scale,
                                                         out_host, ws, s, uniform=True)
         return _lib.GraphedCall(make) if graph else make(stream)
+
+
+class BlockKVCache:
+    """The 8-bit block-scaled cache: int8 or e4m3 codes with one fp32 scale for each block of
+    tokens of a kv head, unrotated (q8 in include/tq.h).  The calls of Int4KVCache, and
+    attend() for several query tokens per sequence (a prefill chunk, drafted tokens).
+
+    head_dim 64, 96, 128 or 256; block 16, 32, 64 or 128 tokens; dtype torch.int8 or
+    torch.float8_e4m3fn.  Calls use no state but the codes and scales: each allocates its
+    workspace on the stream it runs on unless one is passed, so calls on several streams and
+    captured graphs do not share any."""
+
+    def __init__(self, batch: int, num_kv_heads: int, head_dim: int, capacity: int, block: int = 64,
+                 dtype: torch.dtype = torch.int8, device="cuda"):
+        if head_dim not in (64, 96, 128, 256):
+            raise ValueError("head_dim must be 64, 96, 128 or 256")
+        if block not in (16, 32, 64, 128):
+            raise ValueError("block must be 16, 32, 64 or 128")
+        if dtype not in (torch.int8, torch.float8_e4m3fn):
+            raise ValueError("dtype must be torch.int8 or torch.float8_e4m3fn")
+        self.batch, self.num_kv_heads, self.head_dim, self.capacity = batch, num_kv_heads, head_dim, capacity
+        self.block = block
+        dev = torch.device(device)
+        shape = (batch, num_kv_heads, capacity, head_dim)
+        self.k_codes = torch.zeros(shape, dtype=torch.uint8, device=dev).view(dtype)
+        self.v_codes = torch.zeros(shape, dtype=torch.uint8, device=dev).view(dtype)
+        blocks = -(-capacity // block)
+        self.k_scales = torch.zeros(batch, num_kv_heads, blocks, dtype=torch.float32, device=dev)
+        self.v_scales = torch.zeros(batch, num_kv_heads, blocks, dtype=torch.float32, device=dev)
+
+    @property
+    def buffers(self):
+        return self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.block
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k_codes, self.v_codes, self.k_scales, self.v_scales))
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+               n_valid: torch.Tensor | None = None, stream=None) -> None:
+        """Quantize k, v [B][Hkv][n][d] into rows pos[b] .. pos[b]+n-1 (of sequence b only the
+        first n_valid[b] tokens, where n_valid is given)."""
+        _lib.quantize_append_q8(k, v, pos, *self.buffers, n_valid=n_valid, stream=stream)
+
+    def read(self, pos: torch.Tensor | None, rows: int, n_valid: torch.Tensor | None = None,
+             dtype=torch.bfloat16, out=None, stream=None):
+        """The values (k, v) [B][Hkv][rows][d] of rows pos[b] .. pos[b]+rows-1 (see read_q8)."""
+        return _lib.read_q8(*self.buffers, pos, rows, n_valid=n_valid, dtype=dtype, out=out, stream=stream)
+
+    def dequantize(self, rows: int, dtype=torch.bfloat16, stream=None):
+        """The values of rows 0 .. rows-1 of every sequence, [B][Hkv][rows][d]."""
+        return self.read(None, rows, dtype=dtype, stream=stream)
+
+    def decode(self, q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int,
+               attn_scale: float | None = None, out: torch.Tensor | None = None, stream=None,
+               workspace: torch.Tensor | None = None):
+        """Attention of q [B][Hq][d] over rows 0..ctx_lens[b]-1; returns [B][Hq][d], fp32 unless
+        out is given."""
+        return _lib.sdpa_q8_decode(q, *self.buffers, ctx_lens, max_ctx, attn_scale=attn_scale, out=out,
+                                   workspace=workspace, stream=stream)
+
+    def decode_lse(self, q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int, attn_scale: float,
+                   out: torch.Tensor, lse: torch.Tensor, stream=None,
+                   workspace: torch.Tensor | None = None):
+        """decode that also writes each head's softmax state lse[B][Hq][2]."""
+        return _lib.sdpa_q8_decode(q, *self.buffers, ctx_lens, max_ctx, attn_scale=attn_scale, out=out,
+                                   lse=lse, workspace=workspace, stream=stream)
+
+    def decode_append(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                      ctx_lens: torch.Tensor, max_ctx: int, attn_scale: float | None = None,
+                      out: torch.Tensor | None = None, stream=None,
+                      workspace: torch.Tensor | None = None):
+        """One decode step: append k_new, v_new [B][Hkv][1][d] at row ctx_lens[b]-1, then
+        attend q [B][Hq][d] over rows 0..ctx_lens[b]-1 (lengths include the new token)."""
+        return _lib.sdpa_q8_decode_append(q, k_new, v_new, *self.buffers, ctx_lens, max_ctx,
+                                          attn_scale=attn_scale, out=out, workspace=workspace, stream=stream)
+
+    def attend(self, q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int,
+               q_lens: torch.Tensor | None = None, attn_scale: float | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
+               workspace: torch.Tensor | None = None):
+        """Causal attention of each sequence's newest tokens, already appended: query i of
+        q [B][Hq][n][d] sits at position ctx_lens[b] - q_lens[b] + i (see sdpa_q8); returns
+        [B][Hq][n][d] of q's dtype unless out is given."""
+        return _lib.sdpa_q8(q, *self.buffers, ctx_lens, max_ctx, q_lens=q_lens, attn_scale=attn_scale,
+                            out=out, lse=lse, workspace=workspace, stream=stream)

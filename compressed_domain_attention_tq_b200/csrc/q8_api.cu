@@ -1,0 +1,233 @@
+// q8_api.cu -- the C ABI of the 8-bit block-scaled cache (declared in
+// include/tq.h): host-side validation, the split plan, kernel dispatch.
+#include <limits.h>
+#include <math.h>
+#include <stdio.h>
+#include <stdlib.h>
+
+#include "q8_internal.h"
+
+namespace tq {
+
+bool q8_head_dim_supported(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
+
+namespace {
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool misaligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
+
+tq_status status_of(cudaError_t e, const char* where) {
+  if (e == cudaSuccess) return TQ_OK;
+  if (getenv("TQ_DEBUG")) fprintf(stderr, "libtq: %s: %s\n", where, cudaGetErrorString(e));
+  return TQ_ERR_CUDA;
+}
+
+// The checks every call makes of its cache; fills *c.
+tq_status check_cache(const void* k_codes, const float* k_scales, const void* v_codes,
+                      const float* v_scales, int64_t capacity, int32_t batch, int32_t num_kv_heads,
+                      int32_t head_dim, tq_q8_format format, int32_t block, Q8Cache* c) {
+  if (!k_codes || !k_scales || !v_codes || !v_scales) return TQ_ERR_INVALID_ARG;
+  if (format != TQ_Q8_INT8 && format != TQ_Q8_E4M3) return TQ_ERR_INVALID_ARG;
+  if (batch < 1 || num_kv_heads < 1 || capacity < 1) return TQ_ERR_INVALID_ARG;
+  if ((int64_t)batch * num_kv_heads > INT32_MAX) return TQ_ERR_INVALID_ARG;
+  if (!q8_head_dim_supported(head_dim)) return TQ_ERR_UNSUPPORTED;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return TQ_ERR_UNSUPPORTED;
+  if (misaligned(k_codes, 16) || misaligned(v_codes, 16) || misaligned(k_scales, 4) ||
+      misaligned(v_scales, 4))
+    return TQ_ERR_INVALID_ARG;
+  c->k_codes = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+  c->v_codes = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+  c->k_scales = const_cast<float*>(k_scales);
+  c->v_scales = const_cast<float*>(v_scales);
+  c->capacity = capacity;
+  c->B = batch;
+  c->Hkv = num_kv_heads;
+  c->d = head_dim;
+  c->block = block;
+  c->e4m3 = format == TQ_Q8_E4M3;
+  return TQ_OK;
+}
+
+}  // namespace
+
+// Chunks of the context for one call: the count that minimises
+// (waves of work items over the resident CTAs) x (steps of one item + a fixed
+// cost per item, in tokens).  A call whose rows alone fill the GPU is not split.
+bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, int bf16_out, Q8Plan* p) {
+  if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || n < 1 || max_ctx < 1) return false;
+  if (!q8_head_dim_supported(d)) return false;
+  const int64_t G = Hq / Hkv, rows = G * n;
+  if (rows > INT32_MAX / 2 || (int64_t)B * Hkv > INT32_MAX || (int64_t)B * Hq * n > INT32_MAX) return false;
+  (void)bf16_out;
+  p->tensor_memory = 0;
+  p->row_tile = rows <= 8 ? 8 : 16;
+  p->tiles = (int)ceil_div(rows, p->row_tile);
+  const int64_t units = (int64_t)B * Hkv * p->tiles, slots = q8_split_slots(d, p->row_tile);
+  constexpr int64_t kChunkStep = 64, kItemCost = 256;
+  int64_t best = ceil_div(max_ctx, kChunkStep) * kChunkStep, best_cost = -1;
+  for (int64_t k = 1; k <= ceil_div(max_ctx, kChunkStep) && k <= 1024; ++k) {
+    const int64_t chunk = ceil_div(ceil_div(max_ctx, k), kChunkStep) * kChunkStep;
+    const int64_t items = units * ceil_div(max_ctx, chunk);
+    const int64_t cost = ceil_div(items, slots) * (chunk + kItemCost);
+    if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk;
+    if (units * k > 4 * slots) break;
+  }
+  if (best > INT32_MAX) best = INT32_MAX / kChunkStep * kChunkStep;
+  p->chunk = (int)best;
+  p->n_chunks = (int)ceil_div(max_ctx, best);
+  p->part_stride = d + 4;
+  p->header_bytes = (size_t)ceil_div(4LL * B, 256) * 256;
+  p->ws_bytes = p->header_bytes;
+  if (p->n_chunks > 1)
+    p->ws_bytes += sizeof(float) * (size_t)B * Hq * n * p->n_chunks * p->part_stride;
+  return units * p->n_chunks <= INT32_MAX;
+}
+
+namespace {
+
+tq_status attend(const void* q, tq_dtype q_dtype, int32_t num_q_heads, int32_t n, const Q8Cache& c,
+                 const int32_t* ctx_lens, const int32_t* q_lens, int32_t max_ctx, float attn_scale,
+                 void* out, tq_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                 cudaStream_t stream, const Q8WriteArgs* append, const char* where) {
+  if (!q || !ctx_lens || !out) return TQ_ERR_INVALID_ARG;
+  if ((q_dtype != TQ_F32 && q_dtype != TQ_BF16) || (out_dtype != TQ_F32 && out_dtype != TQ_BF16))
+    return TQ_ERR_INVALID_ARG;
+  if (num_q_heads < c.Hkv || num_q_heads % c.Hkv != 0 || n < 1) return TQ_ERR_INVALID_ARG;
+  if (max_ctx < 1 || c.capacity < max_ctx) return TQ_ERR_INVALID_ARG;
+  if (!(attn_scale > 0.0f) || !isfinite(attn_scale)) return TQ_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(out, 16) || misaligned(lse, 8) || misaligned(ctx_lens, 4) ||
+      misaligned(q_lens, 4))
+    return TQ_ERR_INVALID_ARG;
+  Q8AttendArgs a;
+  if (!make_q8_plan(c.B, num_q_heads, c.Hkv, c.d, n, max_ctx, out_dtype == TQ_BF16, &a.plan))
+    return TQ_ERR_INVALID_ARG;
+  if (!workspace || misaligned(workspace, 16) || workspace_bytes < a.plan.ws_bytes)
+    return TQ_ERR_WORKSPACE;
+  a.c = c;
+  a.q = q;
+  a.q_bf16 = q_dtype == TQ_BF16;
+  a.Hq = num_q_heads;
+  a.n = n;
+  a.ctx_lens = ctx_lens;
+  a.q_lens = q_lens;
+  a.max_ctx = max_ctx;
+  a.attn_scale = attn_scale;
+  a.out = out;
+  a.out_bf16 = out_dtype == TQ_BF16;
+  a.lse = lse;
+  a.workspace = workspace;
+  cudaError_t e = append ? launch_q8_append(*append, stream) : cudaSuccess;
+  if (e == cudaSuccess) e = launch_q8_split(a, stream);
+  if (e == cudaSuccess && a.plan.n_chunks > 1) e = launch_q8_merge(a, stream);
+  return status_of(e, where);
+}
+
+}  // namespace
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" {
+
+tq_status tq_quantize_append_q8(const void* k, const void* v, tq_dtype in_dtype, int32_t batch,
+                                int32_t num_kv_heads, int32_t n_new, int32_t head_dim,
+                                tq_q8_format format, int32_t block, const int32_t* pos,
+                                const int32_t* n_valid, void* k_codes, float* k_scales,
+                                void* v_codes, float* v_scales, int64_t capacity,
+                                void* cuda_stream) {
+  Q8WriteArgs a = {};
+  const tq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, capacity, batch, num_kv_heads,
+                                   head_dim, format, block, &a.c);
+  if (st != TQ_OK) return st;
+  if (!k || !v || !pos || n_new < 1 || (in_dtype != TQ_F32 && in_dtype != TQ_BF16))
+    return TQ_ERR_INVALID_ARG;
+  if (misaligned(k, 16) || misaligned(v, 16) || misaligned(pos, 4) || misaligned(n_valid, 4))
+    return TQ_ERR_INVALID_ARG;
+  if (2 * (int64_t)batch * num_kv_heads * (((int64_t)n_new + block - 2) / block + 1) > INT32_MAX ||
+      n_new > INT32_MAX - block)
+    return TQ_ERR_INVALID_ARG;
+  a.k = k;
+  a.v = v;
+  a.bf16 = in_dtype == TQ_BF16;
+  a.n = n_new;
+  a.pos = pos;
+  a.n_valid = n_valid;
+  return status_of(launch_q8_append(a, static_cast<cudaStream_t>(cuda_stream)), "tq_quantize_append_q8");
+}
+
+tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_codes,
+                     const float* v_scales, int64_t capacity, int32_t batch, int32_t num_kv_heads,
+                     int32_t head_dim, tq_q8_format format, int32_t block, const int32_t* pos,
+                     const int32_t* n_valid, int32_t rows, void* k_out, void* v_out,
+                     tq_dtype out_dtype, void* cuda_stream) {
+  Q8ReadArgs a = {};
+  const tq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, capacity, batch, num_kv_heads,
+                                   head_dim, format, block, &a.c);
+  if (st != TQ_OK) return st;
+  if (!k_out || !v_out || rows < 1 || (out_dtype != TQ_F32 && out_dtype != TQ_BF16))
+    return TQ_ERR_INVALID_ARG;
+  if (misaligned(k_out, 16) || misaligned(v_out, 16) || misaligned(pos, 4) || misaligned(n_valid, 4))
+    return TQ_ERR_INVALID_ARG;
+  if (2 * (int64_t)batch * num_kv_heads * ((int64_t)rows / 16 + 1) > INT32_MAX) return TQ_ERR_INVALID_ARG;
+  a.k = k_out;
+  a.v = v_out;
+  a.bf16 = out_dtype == TQ_BF16;
+  a.n = rows;
+  a.pos = pos;
+  a.n_valid = n_valid;
+  return status_of(launch_q8_read(a, static_cast<cudaStream_t>(cuda_stream)), "tq_read_q8");
+}
+
+size_t tq_sdpa_q8_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t n_q, int32_t max_ctx,
+                                  tq_dtype out_dtype) {
+  Q8Plan p;
+  if (!make_q8_plan(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx, out_dtype == TQ_BF16, &p))
+    return 0;
+  return p.ws_bytes;
+}
+
+tq_status tq_sdpa_q8(const void* q, tq_dtype q_dtype, int32_t batch, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t n_q, int32_t head_dim, tq_q8_format format,
+                     int32_t block, const void* k_codes, const float* k_scales, const void* v_codes,
+                     const float* v_scales, int64_t capacity, const int32_t* ctx_lens,
+                     const int32_t* q_lens, int32_t max_ctx, float attn_scale, void* out,
+                     tq_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                     void* cuda_stream) {
+  Q8Cache c;
+  const tq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, capacity, batch, num_kv_heads,
+                                   head_dim, format, block, &c);
+  if (st != TQ_OK) return st;
+  return attend(q, q_dtype, num_q_heads, n_q, c, ctx_lens, q_lens, max_ctx, attn_scale, out, out_dtype,
+                lse, workspace, workspace_bytes, static_cast<cudaStream_t>(cuda_stream), nullptr,
+                "tq_sdpa_q8");
+}
+
+tq_status tq_sdpa_q8_decode_append(
+    const void* q, tq_dtype q_dtype, const void* k_new, const void* v_new, tq_dtype kv_dtype,
+    int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, tq_q8_format format,
+    int32_t block, void* k_codes, float* k_scales, void* v_codes, float* v_scales, int64_t capacity,
+    const int32_t* ctx_lens, int32_t max_ctx, float attn_scale, void* out, tq_dtype out_dtype,
+    float* lse, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  Q8WriteArgs w = {};
+  const tq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, capacity, batch, num_kv_heads,
+                                   head_dim, format, block, &w.c);
+  if (st != TQ_OK) return st;
+  if (!k_new || !v_new || (kv_dtype != TQ_F32 && kv_dtype != TQ_BF16)) return TQ_ERR_INVALID_ARG;
+  if (misaligned(k_new, 16) || misaligned(v_new, 16)) return TQ_ERR_INVALID_ARG;
+  if (2 * (int64_t)batch * num_kv_heads > INT32_MAX) return TQ_ERR_INVALID_ARG;
+  w.k = k_new;
+  w.v = v_new;
+  w.bf16 = kv_dtype == TQ_BF16;
+  w.n = 1;
+  w.pos = ctx_lens;
+  w.pos_is_ctx = 1;
+  w.max_ctx = max_ctx;
+  return attend(q, q_dtype, num_q_heads, 1, w.c, ctx_lens, nullptr, max_ctx, attn_scale, out, out_dtype,
+                lse, workspace, workspace_bytes, static_cast<cudaStream_t>(cuda_stream), &w,
+                "tq_sdpa_q8_decode_append");
+}
+
+}  // extern "C"

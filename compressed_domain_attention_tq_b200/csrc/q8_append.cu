@@ -1,0 +1,264 @@
+// q8_append.cu -- writing tokens into the 8-bit block-scaled cache, and
+// reading a range of it back.
+//
+// Writing.  One CTA owns one block of one kv head's K or V, so the block's new
+// scale and every code that changes with it are decided in one place:
+//   a     = max finite |x| over the block's new rows,  s_new = fl32(a / Q)
+//   s     = max(s_old, s_new) if rows of the block before the first new one are
+//           kept, else s_new
+//   code  = R(fl32(x / s)) (R: nearest, halves to even; NaN -> 0, ends saturate)
+//   kept rows, only when s > s_old:  code' = R(fl32(fl32(code s_old) / s))
+// The new rows stay in registers between the maximum and the division, so HBM
+// sees each input once and each code once.  A thread holds four pieces of
+// eight elements (one 16-byte load of bf16, one 8-byte store), which makes the
+// CTA block * d / 32 threads (32 to 1024).  Bound: HBM.
+//
+// Reading is a stream of 8-byte (bf16) or 4-byte (fp32) code loads with one
+// 16-byte store each.  Bound: HBM.
+#include "q8_common.cuh"
+#include "q8_internal.h"
+
+namespace tq {
+namespace {
+
+using namespace q8;
+
+constexpr int kPieces = 4;  // pieces of 8 elements per thread
+
+template <bool BF16>
+struct Piece {
+  uint4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* base, int64_t elem) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) +
+                                                    elem * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "l"(p + i));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    if constexpr (BF16) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    } else {
+      const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* smem) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = (threadIdx.x & 31) < warps ? smem[threadIdx.x & 31] : 0u;
+  return __reduce_max_sync(0xffffffffu, v);
+}
+
+template <typename F, bool BF16>
+__global__ void __launch_bounds__(1024) append_kernel(Q8WriteArgs a, int touched) {
+  __shared__ uint32_t red[2][32];
+  const Q8Cache& c = a.c;
+  const bool is_v = blockIdx.x & 1;
+  const unsigned unit = blockIdx.x >> 1;
+  const int j = unit % touched;  // block of this sequence's window
+  const int bh = unit / touched;
+  const int b = bh / c.Hkv;
+  int pos = a.pos[b], valid = a.n_valid ? a.n_valid[b] : a.n;
+  if (a.pos_is_ctx) pos = min(pos, a.max_ctx) - 1;
+  if (pos < 0 || valid <= 0) return;
+  valid = min(valid, a.n);
+  const int64_t first = (int64_t)(pos / c.block + j) * c.block;  // the block's first row
+  const int64_t stop = min((int64_t)pos + valid, c.capacity);
+  const int new0 = (int)max((int64_t)0, pos - first);           // new rows [new0, new1) of the block
+  const int new1 = (int)min((int64_t)c.block, stop - first);
+  if (new0 >= new1) return;
+
+  const int per_row = c.d >> 3;
+  const void* in = is_v ? a.v : a.k;
+  uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + ((int64_t)bh * c.capacity + first) * c.d;
+  float* scale = (is_v ? c.v_scales : c.k_scales) + (int64_t)bh * c.n_blocks() + first / c.block;
+  // element of the input that corresponds to the block's row 0
+  const int64_t in0 = ((int64_t)bh * a.n + (first - pos)) * c.d;
+  const float s_old = new0 > 0 ? *scale : 0.0f;
+
+  Piece<BF16> x[kPieces];
+  uint32_t top = 0;  // bits of the largest |x|: above 0x7f800000 for NaN
+  const int lo = new0 * per_row, hi = new1 * per_row;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int p = threadIdx.x + i * blockDim.x;
+    if (p >= lo && p < hi)
+      x[i].load(in, in0 + (int64_t)p * 8);
+    else
+      x[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    float v[8];
+    x[i].values(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  }
+  top = block_max(top, red[0]);
+  const bool finite = top < 0x7f800000u;
+  if (!finite) {  // infinities and NaN do not set the scale
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      float v[8];
+      x[i].values(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __float_as_uint(v[e]) & 0x7fffffffu;
+        if (u < 0x7f800000u) top = max(top, u);
+      }
+    }
+    top = block_max(top, red[1]);
+  }
+  const float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(top), F::kMax));
+  const Divider div = Divider::by(s);
+
+  if (finite && div.fast) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = threadIdx.x + i * blockDim.x;
+      float v[8];
+      x[i].values(v);
+      float y[2][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = div.quick(v[e]);
+      if (p >= lo && p < hi)
+        *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = make_uint2(F::codes4(y[0]), F::codes4(y[1]));
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = threadIdx.x + i * blockDim.x;
+      if (p < lo || p >= hi) continue;
+      Piece<BF16> again;  // re-read: a block with such values is rare
+      again.load(in, in0 + (int64_t)p * 8);
+      float v[8];
+      again.values(v);
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e >> 2] |= F::code(div.any(v[e])) << (8 * (e & 3));
+      *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = make_uint2(w[0], w[1]);
+    }
+  }
+  if (new0 > 0 && s > s_old) {  // the kept rows' codes move to the larger scale
+    for (int p = threadIdx.x; p < lo; p += blockDim.x) {
+      uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)p * 8);
+      const uint2 old = *at;
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[e >> 2] |= F::code(div.any(F::value(e < 4 ? old.x : old.y, e & 3) * s_old)) << (8 * (e & 3));
+      *at = make_uint2(w[0], w[1]);
+    }
+  }
+  if (threadIdx.x == 0) *scale = s;
+}
+
+// -------------------------------------------------------------------- reading
+
+constexpr int kReadThreads = 256, kReadPieces = 4;
+
+// A piece is what one 16-byte store holds: 8 bf16 or 4 fp32 values.
+template <typename F, bool BF16>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(Q8ReadArgs a, int row_tiles, int tile_rows,
+                                                              unsigned row_magic, int block_shift) {
+  const Q8Cache& c = a.c;
+  const bool is_v = blockIdx.x & 1;
+  const unsigned unit = blockIdx.x >> 1;
+  const int tile = unit % row_tiles, bh = unit / row_tiles, b = bh / c.Hkv;
+  const int pos = a.pos ? a.pos[b] : 0;
+  if (pos < 0) return;
+  const int row0 = tile * tile_rows;
+  int64_t rows = min(a.n_valid ? a.n_valid[b] : a.n, a.n);
+  rows = min(min(rows, c.capacity - pos) - row0, (int64_t)tile_rows);
+  if (rows <= 0) return;
+  constexpr int E = BF16 ? 8 : 4;
+  const int per_row = c.d / E, pieces = (int)rows * per_row;
+  const uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + ((int64_t)bh * c.capacity + pos + row0) * c.d;
+  const float* scales = (is_v ? c.v_scales : c.k_scales) + (int64_t)bh * c.n_blocks();
+  unsigned char* out = static_cast<unsigned char*>(is_v ? a.v : a.k) +
+                       ((int64_t)bh * a.n + row0) * c.d * (BF16 ? 2 : 4);
+  const int first = pos + row0;
+  for (int p0 = threadIdx.x; p0 < pieces; p0 += kReadThreads * kReadPieces) {
+    uint32_t w[kReadPieces][2];
+    float s[kReadPieces];
+#pragma unroll
+    for (int i = 0; i < kReadPieces; ++i) {
+      const int p = p0 + i * kReadThreads;
+      if (p >= pieces) continue;
+      s[i] = scales[(first + (int)__umulhi(p, row_magic)) >> block_shift];
+      if constexpr (BF16) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes) + p);
+        w[i][0] = v.x;
+        w[i][1] = v.y;
+      } else {
+        w[i][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes) + p);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kReadPieces; ++i) {
+      const int p = p0 + i * kReadThreads;
+      if (p >= pieces) continue;
+      uint4 o;
+      if constexpr (BF16) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = s[i] * F::value(w[i][e >> 2], e & 3);
+        o = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+      } else {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __float_as_uint(s[i] * F::value(w[i][0], e));
+        o = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      __stcs(reinterpret_cast<uint4*>(out) + p, o);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q8_append(const Q8WriteArgs& a, cudaStream_t stream) {
+  const int touched = (a.n + a.c.block - 2) / a.c.block + 1;  // most blocks n rows can lie in
+  const unsigned grid = 2u * a.c.B * a.c.Hkv * touched;
+  const int threads = (a.c.block * a.c.d / (8 * kPieces) + 31) / 32 * 32;
+  auto* kernel = a.c.e4m3 ? (a.bf16 ? append_kernel<E4m3, true> : append_kernel<E4m3, false>)
+                          : (a.bf16 ? append_kernel<Int8, true> : append_kernel<Int8, false>);
+  kernel<<<grid, threads, 0, stream>>>(a, touched);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t stream) {
+  const int elems = a.bf16 ? 8 : 4;
+  int tile_rows = kReadThreads * kReadPieces * elems / a.c.d;
+  if (tile_rows > a.n) tile_rows = a.n;
+  const int row_tiles = (a.n + tile_rows - 1) / tile_rows;
+  const unsigned grid = 2u * a.c.B * a.c.Hkv * row_tiles;
+  auto* kernel = a.c.e4m3 ? (a.bf16 ? read_kernel<E4m3, true> : read_kernel<E4m3, false>)
+                          : (a.bf16 ? read_kernel<Int8, true> : read_kernel<Int8, false>);
+  const unsigned per_row = a.c.d / elems;
+  const unsigned row_magic = (unsigned)(((1ull << 32) + per_row - 1) / per_row);  // p / per_row for p < 2^16
+  kernel<<<grid, kReadThreads, 0, stream>>>(a, row_tiles, tile_rows, row_magic,
+                                            31 - __builtin_clz((unsigned)a.c.block));
+  return cudaGetLastError();
+}
+
+}  // namespace tq

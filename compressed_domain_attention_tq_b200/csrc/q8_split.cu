@@ -1,0 +1,495 @@
+// q8_split.cu -- attention over the 8-bit block-scaled cache for few query rows
+// per kv head (decode, drafted tokens), and for fp32 outputs of any length.
+//
+// Rows.  The query rows of a kv head are its n tokens x G query heads, row
+// r = i G + g.  A work item is (sequence, kv head, tile of 8 NT rows, chunk of
+// the context); a CTA of four warps takes one, its warps every fourth step of
+// 16 tokens.  16 tokens never cross a block, so a step has one scale of K and
+// one of V.
+//
+// A step is two products on the warp-level tensor cores (m16n8k16, f16 in,
+// fp32 sums), both with the cache as the 16-row operand:
+//   S (16 tokens x 8 rows) = K codes (16 x d) . Q^T,
+//   O (16 dims x 8 rows)  += V codes^T (16 dims x 16 tokens) . W.
+// Every byte is loaded from global memory straight into the lane that feeds it
+// to the tensor core: the summed index may be permuted as long as both operands
+// agree, so a lane takes 16 contiguous bytes of a row wherever the fragment
+// wants four pairs.  No shared memory and no barrier is on the way; the next
+// step's K is loaded once this step's S is done, the next V once O is.
+//
+// Precision: codes are exact in f16.  Each query row is scaled by a power of
+// two and split into f16 hi + lo (22 bits), the weights
+// W = 2^(x - m) s_v / ref likewise, so a product costs two instructions and
+// keeps ~2^-22.  x = S s_k scale log2(e); m is a row's reference, moved only
+// when a score exceeds it by 2^8 (then W <= 2^15 stays in f16's range); ref is
+// the largest V scale so far, so W does not leave the range whatever the
+// scales are.  Sums of weights and O are fp32.
+//
+// Bound: HBM for decode (one pass over the codes).  Tiles of 16 rows (NT = 2)
+// convert a code once for two products; they are taken when a kv head has more
+// than 8 rows.
+#include <limits.h>
+#include <math.h>
+
+#include "q8_common.cuh"
+#include "q8_internal.h"
+
+namespace tq {
+namespace {
+
+using namespace q8;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kStep = 16;
+constexpr float kTau = 8.0f;    // how far (log2) a score may exceed the reference
+constexpr float kShift = 7.0f;  // weights are kept 2^kShift larger: 2^(kTau + kShift) < 65504
+
+// Byte offsets in a row of d codes.  K: word w (0 .. d/16 - 1) of lane t of 4;
+// V: word w (0 .. d/32 - 1) of lane g of 8.  Whole 16-byte loads where d allows.
+template <int D>
+__device__ __forceinline__ int k_offset(int w, int t) {
+  constexpr int full = D / 64 * 4;
+  return w < full ? 64 * (w >> 2) + 16 * t + 4 * (w & 3) : 16 * full + 8 * t + 4 * (w - full);
+}
+template <int D>
+__device__ __forceinline__ int v_offset(int w, int g) {
+  if constexpr (D >= 128) return 128 * (w >> 2) + 16 * g + 4 * (w & 3);
+  return w < 2 ? 8 * g + 4 * w : 64 + 4 * g;  // 64, 96
+}
+
+template <int N>
+__device__ __forceinline__ void ld(uint32_t* r, const uint8_t* p) {
+  if constexpr (N == 4)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p));
+  else if constexpr (N == 2)
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+}
+
+template <int D>
+__device__ __forceinline__ void load_k(uint32_t (&r)[D / 16], const uint8_t* row, int t) {
+#pragma unroll
+  for (int w = 0; w + 4 <= D / 16; w += 4) ld<4>(r + w, row + k_offset<D>(w, t));
+  if constexpr (D % 64) ld<2>(r + D / 64 * 4, row + k_offset<D>(D / 64 * 4, t));
+}
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t (&r)[D / 32], const uint8_t* row, int g) {
+  if constexpr (D >= 128) {
+#pragma unroll
+    for (int w = 0; w < D / 32; w += 4) ld<4>(r + w, row + v_offset<D>(w, g));
+  } else {
+    ld<2>(r, row + v_offset<D>(0, g));
+    if constexpr (D == 96) ld<1>(r + 2, row + v_offset<D>(2, g));
+  }
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// f16 hi and lo parts of a pair of fp32
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = tc::f16x2(x, y);
+  const float2 h = f16x2_to_f32(hi);
+  lo = tc::f16x2(x - h.x, y - h.y);
+}
+
+template <int D, int NT>
+struct Smem {
+  uint4 q[NT][D / 16][32];          // query fragments: hi pair 0, hi pair 1, lo pair 0, lo pair 1
+  float crow[8 * NT];               // scale of a row's sums: attn_scale log2(e) 2^-e
+  float m[kWarps][8 * NT], l[kWarps][8 * NT], ref[kWarps];
+  float acc[kWarps][8][D + 4];      // a row tile's sums of each warp (rows padded against bank conflicts)
+};
+
+// One query element in fp32.
+__device__ __forceinline__ float q_elem(const Q8AttendArgs& a, int64_t row, int x) {
+  const int64_t at = row * a.c.d + x;
+  return a.q_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.q)[at] << 16)
+                  : static_cast<const float*>(a.q)[at];
+}
+
+template <typename F, int D, int NT>
+__global__ void __launch_bounds__(kThreads) split_kernel(Q8AttendArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(raw);
+  constexpr int KW = D / 16, VW = D / 32, MT = D / 16;
+  const Q8Cache& c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int chunk_id = blockIdx.x % a.plan.n_chunks;
+  const unsigned unit = blockIdx.x / a.plan.n_chunks;
+  const int tile = unit % a.plan.tiles;
+  const int bh = unit / a.plan.tiles, b = bh / c.Hkv, hk = bh % c.Hkv;
+  const int G = a.Hq / c.Hkv, rows = a.n * G, row0 = tile * 8 * NT;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // a decode step's append comes first
+  const Q8Seq seq(a, b);
+  if (chunk_id == 0 && tile == 0 && hk == 0 && threadIdx.x == 0)
+    static_cast<int32_t*>(a.workspace)[b] = seq.bad;
+
+  const int last_i = min(rows - 1, row0 + 8 * NT - 1) / G;  // the tile's last and first query token
+  const int first_i = row0 / G;
+  const int q_last = min(last_i, seq.q_len - 1);
+  const int stop_all = q_last < first_i ? 0 : seq.limit(q_last);  // rows any of the tile's queries sees
+  const int begin = chunk_id * a.plan.chunk;
+  const int stop = min(stop_all, begin + a.plan.chunk);
+  if (begin >= stop && (chunk_id > 0 || a.plan.n_chunks > 1)) return;
+
+  // -- query fragments, each row scaled so that its largest element is in [2^13, 2^14)
+  for (int r = warp; r < 8 * NT; r += kWarps) {
+    const int i = (row0 + r) / G;
+    const bool live = row0 + r < rows && i < seq.q_len;
+    const int64_t qrow = ((int64_t)b * a.Hq + hk * G + (row0 + r) % G) * a.n + i;
+    float top = 0.0f;
+    if (live)
+      for (int x = lane; x < D; x += 32) top = fmaxf(top, fabsf(q_elem(a, qrow, x)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+    const float up = tc::pow2i(e);
+    const int nt = r >> 3, rg = r & 7;
+    for (int p = lane; p < KW * 4; p += 32) {  // (word, lane of 4)
+      const int w = p >> 2, tt = p & 3, off = k_offset<D>(w, tt);
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          x[k] = q_elem(a, qrow, off + F::place(0, k)) * up;
+          x[2 + k] = q_elem(a, qrow, off + F::place(1, k)) * up;
+        }
+      }
+      uint4 f;
+      split2(x[0], x[1], f.x, f.z);
+      split2(x[2], x[3], f.y, f.w);
+      sm.q[nt][w][rg * 4 + tt] = f;
+    }
+    if (lane == 0) sm.crow[r] = a.attn_scale * kLog2e * tc::pow2i(-e);
+  }
+  __syncthreads();
+
+  // -- this lane's rows of the S and O fragments: 8 nt + 2t, 8 nt + 2t + 1
+  float crow[NT][2], m[NT][2], l[NT][2];
+  int limit[NT][2];
+  int open = stop;  // tokens below this are seen by every row of the tile
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 8 * nt + 2 * t + k, i = (row0 + r) / G;
+      crow[nt][k] = sm.crow[r];
+      limit[nt][k] = row0 + r < rows && i < seq.q_len ? seq.limit(i) : INT_MAX;  // rows of no query: ignored
+      open = min(open, limit[nt][k]);
+      m[nt][k] = -INFINITY;
+      l[nt][k] = 0.0f;
+    }
+  open = __reduce_min_sync(0xffffffffu, open);
+  float acc[NT][MT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.0f;
+  float ref = 0.0f;
+
+  const uint8_t* kc = c.k_codes + (int64_t)bh * c.capacity * D;
+  const uint8_t* vc = c.v_codes + (int64_t)bh * c.capacity * D;
+  const float* ksc = c.k_scales + (int64_t)bh * c.n_blocks();
+  const float* vsc = c.v_scales + (int64_t)bh * c.n_blocks();
+  const int shift = 31 - __clz(c.block);
+
+  uint32_t kr[2][KW], vr[4][VW];
+  float ks = 0.0f, vs = 0.0f;
+  // rows behind the last one repeat it, so what a lane multiplies is always cache content
+  auto k_rows = [&](int tok) {
+    load_k<D>(kr[0], kc + (int64_t)min(tok + g, stop - 1) * D, t);
+    load_k<D>(kr[1], kc + (int64_t)min(tok + g + 8, stop - 1) * D, t);
+    ks = __ldg(ksc + (tok >> shift));
+  };
+  auto v_rows = [&](int tok) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      load_v<D>(vr[j], vc + (int64_t)min(tok + 2 * t + (j & 1) + 8 * (j >> 1), stop - 1) * D, g);
+    vs = __ldg(vsc + (tok >> shift));
+  };
+
+  int tok = begin + kStep * warp;
+  if (tok < stop) {
+    k_rows(tok);
+    v_rows(tok);
+  }
+  for (; tok < stop; tok += kStep * kWarps) {
+    const int next = tok + kStep * kWarps;
+    float s[NT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nt][0][j] = s[nt][1][j] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      uint32_t f[4];
+      F::cvt_word(kr[0][w], f[0], f[2]);
+      F::cvt_word(kr[1][w], f[1], f[3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 q = sm.q[nt][w][lane];
+        mma(s[nt][0], f, q.x, q.y);
+        mma(s[nt][1], f, q.z, q.w);
+      }
+    }
+    const float ks_now = ks;
+    if (next < stop) k_rows(next);
+
+    if (vs > ref) {  // warp-uniform: a larger V scale becomes the reference
+      const float down = ref / vs;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nt][i][j] *= down;
+      ref = vs;
+    }
+    const float ratio = ref > 0.0f ? vs / ref : 0.0f;
+    uint32_t whi[NT][2], wlo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = (s[nt][0][j] + s[nt][1][j]) * (ks_now * crow[nt][j & 1]);
+      if (tok + kStep > open) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (tok + g + 8 * (j >> 1) >= limit[nt][j & 1]) x[j] = -INFINITY;
+      }
+      const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
+      const bool move = top0 > m[nt][0] + (kTau + kShift) || top1 > m[nt][1] + (kTau + kShift);
+      if (__any_sync(0xffffffffu, move)) {
+        float top[2] = {top0, top1};
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+        }
+        float alpha[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // m is held 2^kShift low
+          const float mn = fmaxf(m[nt][k], top[k] - kShift);
+          alpha[k] = mn == m[nt][k] ? 1.0f : exp2f(m[nt][k] - mn);
+          m[nt][k] = mn;
+          l[nt][k] *= alpha[k];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nt][i][j] *= alpha[j & 1];
+      }
+      float p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float mm = m[nt][j & 1] == -INFINITY ? 0.0f : m[nt][j & 1];
+        p[j] = tc::ex2(x[j] - mm);
+        l[nt][j & 1] += p[j];
+        p[j] *= ratio;
+      }
+      uint32_t h0, l0, h1, l1;
+      split2(p[0], p[1], h0, l0);
+      split2(p[2], p[3], h1, l1);
+      whi[nt][0] = transpose8(h0);
+      whi[nt][1] = transpose8(h1);
+      wlo[nt][0] = transpose8(l0);
+      wlo[nt][1] = transpose8(l1);
+    }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      uint32_t f01[4], f23[4];  // bytes 0..3 for tokens (2t, 2t+1) and (2t+8, 2t+9)
+      F::cvt_two(vr[0][w], vr[1][w], f01);
+      F::cvt_two(vr[2][w], vr[3][w], f23);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t f[4] = {f01[2 * h], f01[2 * h + 1], f23[2 * h], f23[2 * h + 1]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma(acc[nt][2 * w + h], f, whi[nt][0], whi[nt][1]);
+          mma(acc[nt][2 * w + h], f, wlo[nt][0], wlo[nt][1]);
+        }
+      }
+    }
+    if (next < stop) v_rows(next);
+  }
+
+  // -- join the warps: sums over the lanes of a row, then over the warps
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
+      if (g == 0) {
+        sm.m[warp][8 * nt + 2 * t + k] = m[nt][k];
+        sm.l[warp][8 * nt + 2 * t + k] = l[nt][k];
+      }
+    }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (nt > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int byte = 2 * i + (j >> 1);  // byte of this lane's part of a V row
+        sm.acc[warp][2 * t + (j & 1)][v_offset<D>(byte >> 2, g) + (byte & 3)] = acc[nt][i][j] * ref;
+      }
+    __syncthreads();
+    for (int p = threadIdx.x; p < 8 * (D / 4); p += kThreads) {
+      const int rr = p / (D / 4), x = p % (D / 4) * 4, r = 8 * nt + rr;
+      const int i = (row0 + r) / G;
+      if (row0 + r >= rows || i >= seq.q_len) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][r]);
+      const float base = M == -INFINITY ? 0.0f : M;
+      float L = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(sm.m[w][r] - base);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.acc[w][rr][x]);
+        L = fmaf(f, sm.l[w][r], L);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      const int64_t orow = ((int64_t)b * a.Hq + hk * G + (row0 + r) % G) * a.n + i;
+      if (a.plan.n_chunks > 1) {
+        float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + a.plan.header_bytes) +
+                      (orow * a.plan.n_chunks + chunk_id) * a.plan.part_stride;
+        *reinterpret_cast<float4*>(part + x) = o;
+        if (x == 0) *reinterpret_cast<float2*>(part + D) = make_float2(M, L);
+        continue;
+      }
+      const bool none = M == -INFINITY && L == 0.0f;  // no row seen
+      const float inv = none ? 0.0f : 1.0f / L;
+      o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      if (a.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + x) =
+            make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) = o;
+      if (a.lse != nullptr && x == 0) *reinterpret_cast<float2*>(a.lse + orow * 2) = make_float2(M, L);
+    }
+  }
+}
+
+// Joins the chunks of each query row: with M = max m_c, o = sum 2^(m_c - M)
+// acc_c / sum 2^(m_c - M) l_c.  One warp per 128 (bf16 or fp32) output
+// elements, a lane four of them.  The launch is the split kernel's programmatic
+// dependent, so its start overlaps the split's tail.
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int d = a.c.d, pieces = (d + 127) / 128;
+  const int64_t id = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int64_t orow = id / pieces;
+  if (orow >= (int64_t)a.c.B * a.Hq * a.n) return;
+  const int x = (int)(id % pieces) * 128 + 4 * lane;
+  const int b = (int)(orow / ((int64_t)a.Hq * a.n)), i = (int)(orow % a.n);
+  const Q8Seq seq(a, b);
+  if (i >= seq.q_len) return;
+  const int nc = (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk;
+  const float* part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.workspace) +
+                                                     a.plan.header_bytes) +
+                      orow * a.plan.n_chunks * a.plan.part_stride;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float M = -INFINITY;
+  for (int k = lane; k < nc; k += 32) M = fmaxf(M, part[(int64_t)k * a.plan.part_stride + d]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < nc; ++k) {
+    const float* p = part + (int64_t)k * a.plan.part_stride;
+    const float2 ml = *reinterpret_cast<const float2*>(p + d);
+    const float4 v = x < d ? *reinterpret_cast<const float4*>(p + x) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float f = exp2f(ml.x - base);
+    L = fmaf(f, ml.y, L);
+    o.x = fmaf(f, v.x, o.x);
+    o.y = fmaf(f, v.y, o.y);
+    o.z = fmaf(f, v.z, o.z);
+    o.w = fmaf(f, v.w, o.w);
+  }
+  const float inv = nc == 0 ? 0.0f : 1.0f / L;
+  if (x < d) {
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (a.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * d + x) =
+          make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * d + x) = o;
+  }
+  if (a.lse != nullptr && x == 0) *reinterpret_cast<float2*>(a.lse + orow * 2) = make_float2(M, L);
+}
+
+template <typename F, int D, int NT>
+cudaError_t launch_one(const Q8AttendArgs& a, cudaStream_t stream) {
+  static SmemLimitSet done;
+  constexpr int bytes = sizeof(Smem<D, NT>);
+  const cudaError_t e = ensure_smem_limit(split_kernel<F, D, NT>, bytes, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = (int64_t)a.c.B * a.c.Hkv * a.plan.tiles * a.plan.n_chunks;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, split_kernel<F, D, NT>, a);
+}
+
+template <typename F>
+cudaError_t launch_format(const Q8AttendArgs& a, cudaStream_t stream) {
+  const bool two = a.plan.row_tile == 16;
+  switch (a.c.d) {
+    case 64: return two ? launch_one<F, 64, 2>(a, stream) : launch_one<F, 64, 1>(a, stream);
+    case 96: return two ? launch_one<F, 96, 2>(a, stream) : launch_one<F, 96, 1>(a, stream);
+    case 128: return two ? launch_one<F, 128, 2>(a, stream) : launch_one<F, 128, 1>(a, stream);
+    default: return two ? launch_one<F, 256, 2>(a, stream) : launch_one<F, 256, 1>(a, stream);
+  }
+}
+
+}  // namespace
+
+int q8_split_slots(int d, int row_tile) { return kSmCount * (d == 256 && row_tile == 16 ? 2 : 3); }
+
+cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream) {
+  return a.c.e4m3 ? launch_format<E4m3>(a, stream) : launch_format<Int8>(a, stream);
+}
+
+cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
+  const int64_t warps = (int64_t)a.c.B * a.Hq * a.n * ((a.c.d + 127) / 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_q8_kernel, a);
+}
+
+}  // namespace tq

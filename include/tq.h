@@ -529,6 +529,121 @@ TQ_API tq_status tq_sdpa_uniform_decode_append_host(
     size_t workspace_bytes, void* cuda_stream);
 
 /*
+ * The 8-bit block-scaled cache ("q8"): K and V as 8-bit codes with one fp32
+ * scale for each block of `block` consecutive tokens of a kv head, unrotated.
+ * It stands beside the caches above for uses that want more than one query
+ * token at a time, narrower heads, or the higher precision of 8 bits.
+ *
+ * Layout (row-major, dense):
+ *  - codes: 1 byte each, [B][Hkv][capacity][d], int8 in [-127, 127] or e4m3;
+ *  - scales: float [B][Hkv][ceil(capacity / block)];
+ *  - value = fl32(scale * code).
+ * head_dim d in {64, 96, 128, 256}; block in {16, 32, 64, 128}; codes, q, k, v
+ * and outputs 16-byte aligned.  Any Hq / Hkv.  The conventions at the top of
+ * this file hold (no allocation, no synchronization, deterministic results).
+ */
+typedef enum { TQ_Q8_INT8 = 0, TQ_Q8_E4M3 = 1 } tq_q8_format;
+
+/*
+ * tq_quantize_append_q8 -- quantize tokens of K and V as they are written into
+ * cache rows pos[b] .. pos[b] + n - 1 of each sequence.  With Q = 127 (int8) or
+ * 448 (e4m3), each block of each kv head that receives rows gets
+ *     s = max(s_old, fl32(a / Q)),  a = the largest finite |x| of its new rows,
+ * (s_old counts only when rows of the block in front of pos[b] are kept), and
+ * every new element the code R(fl32(x / s)), R rounding to the nearest code,
+ * halves to even.  Infinities saturate, NaN is stored as 0, a block of zeros
+ * has scale 0.  When a new row raises a block's scale, the codes of the rows
+ * kept in it move to the new scale: R(fl32(fl32(code * s_old) / s)).  Rows
+ * behind the last written one are left as they were, and belong to no
+ * sequence: a later append at a smaller pos overwrites (drafted tokens that
+ * were rejected).
+ *
+ *  k, v      [B][Hkv][n_new][d] of in_dtype (fp32 or bf16).
+ *  pos       device int32 [B]; a sequence with pos[b] < 0 is skipped, rows
+ *            pos[b] + i >= capacity are skipped.
+ *  n_valid   device int32 [B] or NULL: only the first n_valid[b] (clamped to
+ *            [0, n_new]) tokens of sequence b are written.
+ * Returns TQ_ERR_INVALID_ARG for NULL pointers (other than n_valid), sizes < 1
+ * or beyond 2^31 - 1 work items, misaligned pointers, unknown types;
+ * TQ_ERR_UNSUPPORTED for a head_dim or block outside the sets above.
+ */
+TQ_API tq_status tq_quantize_append_q8(
+    const void* k, const void* v, tq_dtype in_dtype, int32_t batch, int32_t num_kv_heads,
+    int32_t n_new, int32_t head_dim, tq_q8_format format, int32_t block, const int32_t* pos,
+    const int32_t* n_valid, void* k_codes, float* k_scales, void* v_codes, float* v_scales,
+    int64_t capacity, void* cuda_stream);
+
+/*
+ * tq_read_q8 -- the values of cache rows pos[b] .. pos[b] + rows - 1 of each
+ * sequence, K and V in one launch: k_out, v_out [B][Hkv][rows][d] of out_dtype
+ * (fp32: fl32(scale * code); bf16: that rounded once).
+ *  pos       device int32 [B], or NULL for 0.
+ *  n_valid   device int32 [B] or NULL: only the first n_valid[b] rows.
+ * Outputs of rows outside the cache (pos[b] + i >= capacity, pos[b] < 0) or at
+ * n_valid[b] and behind are left as they were.  Errors as tq_quantize_append_q8.
+ */
+TQ_API tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_codes,
+                            const float* v_scales, int64_t capacity, int32_t batch,
+                            int32_t num_kv_heads, int32_t head_dim, tq_q8_format format,
+                            int32_t block, const int32_t* pos, const int32_t* n_valid,
+                            int32_t rows, void* k_out, void* v_out, tq_dtype out_dtype,
+                            void* cuda_stream);
+
+/* Bytes of device workspace tq_sdpa_q8 needs for these sizes (host only); 0
+ * for invalid sizes.  tq_sdpa_q8_decode_append needs those of n_q = 1. */
+TQ_API size_t tq_sdpa_q8_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t n_q, int32_t max_ctx,
+                                         tq_dtype out_dtype);
+
+/*
+ * tq_sdpa_q8 -- attention of the newest n_q tokens of each sequence over its
+ * q8 cache (n_q = 1: decode; more: a prefill chunk, or drafted tokens).  The
+ * sequence's ctx_lens[b] rows include the query tokens' own: query i sits at
+ * position ctx_lens[b] - q_lens[b] + i and attends rows 0 .. that position.
+ *
+ *  q         [B][Hq][n_q][d] of q_dtype; Hq % Hkv == 0, query head h attends
+ *            kv head h / (Hq / Hkv).
+ *  ctx_lens  device int32 [B] in [0, max_ctx]; q_lens device int32 [B] in
+ *            [0, n_q], or NULL for n_q.  Values outside are clamped, and every
+ *            call writes int32 flag[b] at the start of the workspace: 1 if one
+ *            of sequence b's was, else 0.
+ *  max_ctx   host bound on ctx_lens; max_ctx <= capacity.
+ *  out       [B][Hq][n_q][d] of out_dtype.  Queries that attend no row (a
+ *            position below 0) get zeros; rows of queries i >= q_lens[b] are
+ *            left as they were.  fp32 outputs are computed with products split
+ *            into two f16 parts (relative error near 1e-6); bf16 outputs of
+ *            long query chunks may be computed with weights of 11 bits (an
+ *            error well below that of the output's own rounding).
+ *  lse       NULL, or float [B][Hq][n_q][2], 8-byte aligned: (M, L) with
+ *            L = sum_t 2^(attn_scale * q.k_t * log2(e) - M), M near the maximum
+ *            (-inf and 0 where nothing is attended).  With n_q = 1 and fp32
+ *            outputs these are parts for tq_merge_lse.
+ *  workspace tq_sdpa_q8_workspace_bytes() bytes, 16-byte aligned.
+ * Errors as tq_sdpa_int4_decode.
+ */
+TQ_API tq_status tq_sdpa_q8(const void* q, tq_dtype q_dtype, int32_t batch, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t n_q, int32_t head_dim,
+                            tq_q8_format format, int32_t block, const void* k_codes,
+                            const float* k_scales, const void* v_codes, const float* v_scales,
+                            int64_t capacity, const int32_t* ctx_lens, const int32_t* q_lens,
+                            int32_t max_ctx, float attn_scale, void* out, tq_dtype out_dtype,
+                            float* lse, void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * tq_sdpa_q8_decode_append -- one decode step: the new token's K and V
+ * [B][Hkv][1][d] are written to row ctx_lens[b] - 1 (as tq_quantize_append_q8
+ * writes them) and q [B][Hq][d] attends rows 0 .. ctx_lens[b] - 1.  Lengths
+ * include the new token; a sequence of length 0 (an empty place in the batch)
+ * writes nothing and gets zeros.
+ */
+TQ_API tq_status tq_sdpa_q8_decode_append(
+    const void* q, tq_dtype q_dtype, const void* k_new, const void* v_new, tq_dtype kv_dtype,
+    int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, tq_q8_format format,
+    int32_t block, void* k_codes, float* k_scales, void* v_codes, float* v_scales, int64_t capacity,
+    const int32_t* ctx_lens, int32_t max_ctx, float attn_scale, void* out, tq_dtype out_dtype,
+    float* lse, void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/*
  * tq_set_test_hooks -- testing only; leave at 0 (the default) in normal use.
  * Sets process-wide switches read once by every later decode or quantize
  * call:
