@@ -121,8 +121,12 @@ __device__ __forceinline__ float q_elem(const Q8AttendArgs& a, int64_t row, int 
                   : static_cast<const float*>(a.q)[at];
 }
 
+// CTAs per SM that the registers of a variant allow (accumulators, the next
+// step's codes and the queries' row state: 64 d NT / 32 + d / 4 + ...).
+constexpr int resident(int d, int nt) { return d == 256 ? 2 : d == 128 ? 5 - nt : nt == 1 ? 5 : 4; }
+
 template <typename F, int D, int NT>
-__global__ void __launch_bounds__(kThreads) split_kernel(Q8AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8AttendArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(raw);
   constexpr int KW = D / 16, VW = D / 32, MT = D / 16;
@@ -394,53 +398,96 @@ __global__ void __launch_bounds__(kThreads) split_kernel(Q8AttendArgs a) {
 }
 
 // Joins the chunks of each query row: with M = max m_c, o = sum 2^(m_c - M)
-// acc_c / sum 2^(m_c - M) l_c.  One warp per 128 (bf16 or fp32) output
-// elements, a lane four of them.  The launch is the split kernel's programmatic
-// dependent, so its start overlaps the split's tail.
-constexpr int kMergeWarps = 4;
+// acc_c / sum 2^(m_c - M) l_c.  One CTA per row, warp w takes the chunks w,
+// w + 8, ... with a lane on every fourth output element, so a row of up to 64
+// chunks is eight independent loads deep; the eight sums meet in shared memory.
+// The launch is the split kernel's programmatic dependent, so its start overlaps
+// the split's tail.
+constexpr int kMergeWarps = 8;
+template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int d = a.c.d, pieces = (d + 127) / 128;
-  const int64_t id = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int64_t orow = id / pieces;
-  if (orow >= (int64_t)a.c.B * a.Hq * a.n) return;
-  const int x = (int)(id % pieces) * 128 + 4 * lane;
+  constexpr int P = (D + 127) / 128;  // pieces of 128 elements
+  __shared__ float4 sums[kMergeWarps][P][32];
+  __shared__ float2 state[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t orow = blockIdx.x;
   const int b = (int)(orow / ((int64_t)a.Hq * a.n)), i = (int)(orow % a.n);
   const Q8Seq seq(a, b);
   if (i >= seq.q_len) return;
-  const int nc = (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk;
+  const int nc = (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk, stride = a.plan.part_stride;
   const float* part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.workspace) +
                                                      a.plan.header_bytes) +
-                      orow * a.plan.n_chunks * a.plan.part_stride;
+                      orow * a.plan.n_chunks * stride;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float M = -INFINITY;
-  for (int k = lane; k < nc; k += 32) M = fmaxf(M, part[(int64_t)k * a.plan.part_stride + d]);
+  float M = -INFINITY, L = 0.0f;  // of this warp's chunks
+  float4 o[P];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int p = 0; p < P; ++p) o[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int U = 4;
+  for (int k0 = warp; k0 < nc; k0 += U * kMergeWarps) {
+    float2 ml[U];
+    float4 v[U][P];
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kMergeWarps;
+      const float* pk = part + (int64_t)k * stride;
+      ml[u] = k < nc ? *reinterpret_cast<const float2*>(pk + D) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        v[u][p] = k < nc && 128 * p + 4 * lane < D ? *reinterpret_cast<const float4*>(pk + 128 * p + 4 * lane)
+                                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float keep = exp2f(M - base);
+    M = top;
+    L *= keep;
+#pragma unroll
+    for (int p = 0; p < P; ++p) o[p] = make_float4(o[p].x * keep, o[p].y * keep, o[p].z * keep, o[p].w * keep);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = exp2f(ml[u].x - base);
+      L = fmaf(f, ml[u].y, L);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        o[p].x = fmaf(f, v[u][p].x, o[p].x);
+        o[p].y = fmaf(f, v[u][p].y, o[p].y);
+        o[p].z = fmaf(f, v[u][p].z, o[p].z);
+        o[p].w = fmaf(f, v[u][p].w, o[p].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) sums[warp][p][lane] = o[p];
+  if (lane == 0) state[warp] = make_float2(M, L);
+  __syncthreads();
+  if (threadIdx.x >= D / 4) return;  // a thread per four output elements
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, state[w].x);
   const float base = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = 0; k < nc; ++k) {
-    const float* p = part + (int64_t)k * a.plan.part_stride;
-    const float2 ml = *reinterpret_cast<const float2*>(p + d);
-    const float4 v = x < d ? *reinterpret_cast<const float4*>(p + x) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float f = exp2f(ml.x - base);
-    L = fmaf(f, ml.y, L);
-    o.x = fmaf(f, v.x, o.x);
-    o.y = fmaf(f, v.y, o.y);
-    o.z = fmaf(f, v.z, o.z);
-    o.w = fmaf(f, v.w, o.w);
+  L = 0.0f;
+  float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = exp2f(state[w].x - base);
+    const float4 v = sums[w][threadIdx.x >> 5][lane];
+    L = fmaf(f, state[w].y, L);
+    r.x = fmaf(f, v.x, r.x);
+    r.y = fmaf(f, v.y, r.y);
+    r.z = fmaf(f, v.z, r.z);
+    r.w = fmaf(f, v.w, r.w);
   }
   const float inv = nc == 0 ? 0.0f : 1.0f / L;
-  if (x < d) {
-    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (a.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * d + x) =
-          make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * d + x) = o;
-  }
+  r = make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
+  const int x = 4 * threadIdx.x;
+  if (a.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + x) =
+        make_uint2(bf16x2(r.x, r.y), bf16x2(r.z, r.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) = r;
   if (a.lse != nullptr && x == 0) *reinterpret_cast<float2*>(a.lse + orow * 2) = make_float2(M, L);
 }
 
@@ -472,16 +519,15 @@ cudaError_t launch_format(const Q8AttendArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int q8_split_slots(int d, int row_tile) { return kSmCount * (d == 256 && row_tile == 16 ? 2 : 3); }
+int q8_split_slots(int d, int row_tile) { return kSmCount * resident(d, row_tile / 8); }
 
 cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream) {
   return a.c.e4m3 ? launch_format<E4m3>(a, stream) : launch_format<Int8>(a, stream);
 }
 
 cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
-  const int64_t warps = (int64_t)a.c.B * a.Hq * a.n * ((a.c.d + 127) / 128);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((warps + kMergeWarps - 1) / kMergeWarps));
+  cfg.gridDim = dim3((unsigned)((int64_t)a.c.B * a.Hq * a.n));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -489,7 +535,12 @@ cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_q8_kernel, a);
+  switch (a.c.d) {
+    case 64: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<64>, a);
+    case 96: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<96>, a);
+    case 128: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<128>, a);
+    default: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<256>, a);
+  }
 }
 
 }  // namespace tq
