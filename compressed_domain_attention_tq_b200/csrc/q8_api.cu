@@ -52,36 +52,58 @@ tq_status check_cache(const void* k_codes, const float* k_scales, const void* v_
 
 }  // namespace
 
+namespace {
+
 // Chunks of the context for one call: the count that minimises
-// (waves of work items over the resident CTAs) x (steps of one item + a fixed
+// (waves of work items over the resident CTAs) x (tokens of one item + a fixed
 // cost per item, in tokens).  A call whose rows alone fill the GPU is not split.
-bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, int bf16_out, Q8Plan* p) {
+void split_context(int64_t units, int64_t slots, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
+  int64_t best = ceil_div(max_ctx, step) * step, best_cost = -1;
+  for (int64_t k = 1; k <= ceil_div(max_ctx, step) && k <= 1024; ++k) {
+    const int64_t chunk = ceil_div(ceil_div(max_ctx, k), step) * step;
+    const int64_t items = units * ceil_div(max_ctx, chunk);
+    const int64_t cost = ceil_div(items, slots) * (chunk + item_cost);
+    if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk;
+    if (units * k > 4 * slots) break;
+  }
+  if (best > INT32_MAX) best = INT32_MAX / step * step;
+  p->chunk = (int)best;
+  p->n_chunks = (int)ceil_div(max_ctx, best);
+}
+
+}  // namespace
+
+// bf16: queries and outputs are bf16.
+bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, Q8Plan* p) {
   if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || n < 1 || max_ctx < 1) return false;
   if (!q8_head_dim_supported(d)) return false;
   const int64_t G = Hq / Hkv, rows = G * n;
   if (rows > INT32_MAX / 2 || (int64_t)B * Hkv > INT32_MAX || (int64_t)B * Hq * n > INT32_MAX) return false;
-  (void)bf16_out;
-  p->tensor_memory = 0;
-  p->row_tile = rows <= 8 ? 8 : 16;
-  p->tiles = (int)ceil_div(rows, p->row_tile);
-  const int64_t units = (int64_t)B * Hkv * p->tiles, slots = q8_split_slots(d, p->row_tile);
-  constexpr int64_t kChunkStep = 64, kItemCost = 256;
-  int64_t best = ceil_div(max_ctx, kChunkStep) * kChunkStep, best_cost = -1;
-  for (int64_t k = 1; k <= ceil_div(max_ctx, kChunkStep) && k <= 1024; ++k) {
-    const int64_t chunk = ceil_div(ceil_div(max_ctx, k), kChunkStep) * kChunkStep;
-    const int64_t items = units * ceil_div(max_ctx, chunk);
-    const int64_t cost = ceil_div(items, slots) * (chunk + kItemCost);
-    if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk;
-    if (units * k > 4 * slots) break;
+  int64_t slots, step, item_cost;
+  if (bf16 && rows > 16) {
+    p->mode = d > 128 ? kQ8OneStream : rows > 128 ? kQ8TwoRows : kQ8TwoStreams;
+    p->row_tile = p->mode == kQ8TwoRows ? 256 : 128;
+    p->parts = p->mode == kQ8TwoStreams ? 2 : 1;
+    slots = kSmCount;
+    step = p->parts * q8_tc_tile_tokens(d);
+    item_cost = 1024;
+  } else {
+    p->mode = kQ8Warps;
+    p->row_tile = rows <= 8 ? 8 : 16;
+    p->parts = 1;
+    slots = q8_split_slots(d, p->row_tile);
+    step = 64;
+    item_cost = 256;
   }
-  if (best > INT32_MAX) best = INT32_MAX / kChunkStep * kChunkStep;
-  p->chunk = (int)best;
-  p->n_chunks = (int)ceil_div(max_ctx, best);
+  p->tiles = (int)ceil_div(rows, p->row_tile);
+  const int64_t units = (int64_t)B * Hkv * p->tiles;
+  split_context(units, slots, max_ctx, step, item_cost, p);
+  p->n_parts = p->n_chunks * p->parts;
   p->part_stride = d + 4;
   p->header_bytes = (size_t)ceil_div(4LL * B, 256) * 256;
   p->ws_bytes = p->header_bytes;
-  if (p->n_chunks > 1)
-    p->ws_bytes += sizeof(float) * (size_t)B * Hq * n * p->n_chunks * p->part_stride;
+  if (p->n_parts > 1)
+    p->ws_bytes += sizeof(float) * (size_t)B * Hq * n * p->n_parts * p->part_stride;
   return units * p->n_chunks <= INT32_MAX;
 }
 
@@ -101,7 +123,7 @@ tq_status attend(const void* q, tq_dtype q_dtype, int32_t num_q_heads, int32_t n
       misaligned(q_lens, 4))
     return TQ_ERR_INVALID_ARG;
   Q8AttendArgs a;
-  if (!make_q8_plan(c.B, num_q_heads, c.Hkv, c.d, n, max_ctx, out_dtype == TQ_BF16, &a.plan))
+  if (!make_q8_plan(c.B, num_q_heads, c.Hkv, c.d, n, max_ctx, q_dtype == TQ_BF16 && out_dtype == TQ_BF16, &a.plan))
     return TQ_ERR_INVALID_ARG;
   if (!workspace || misaligned(workspace, 16) || workspace_bytes < a.plan.ws_bytes)
     return TQ_ERR_WORKSPACE;
@@ -118,9 +140,12 @@ tq_status attend(const void* q, tq_dtype q_dtype, int32_t num_q_heads, int32_t n
   a.out_bf16 = out_dtype == TQ_BF16;
   a.lse = lse;
   a.workspace = workspace;
+  const unsigned hooks = g_test_hooks.load(std::memory_order_relaxed);
+  if (hooks & TQ_TEST_HOOK_FAIL_LAUNCH) return status_of(cudaErrorLaunchFailure, where);
+  a.test_starve = (hooks & TQ_TEST_HOOK_STARVE_PIPELINE) != 0;
   cudaError_t e = append ? launch_q8_append(*append, stream) : cudaSuccess;
-  if (e == cudaSuccess) e = launch_q8_split(a, stream);
-  if (e == cudaSuccess && a.plan.n_chunks > 1) e = launch_q8_merge(a, stream);
+  if (e == cudaSuccess) e = a.plan.mode == kQ8Warps ? launch_q8_split(a, stream) : launch_q8_tc(a, stream);
+  if (e == cudaSuccess && a.plan.n_parts > 1) e = launch_q8_merge(a, stream);
   return status_of(e, where);
 }
 
@@ -183,10 +208,11 @@ tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_c
 size_t tq_sdpa_q8_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                   int32_t head_dim, int32_t n_q, int32_t max_ctx,
                                   tq_dtype out_dtype) {
-  Q8Plan p;
-  if (!make_q8_plan(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx, out_dtype == TQ_BF16, &p))
-    return 0;
-  return p.ws_bytes;
+  Q8Plan p, q;  // bf16 outputs: enough for queries of either type
+  if (!make_q8_plan(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx, false, &p)) return 0;
+  if (out_dtype != TQ_BF16) return p.ws_bytes;
+  if (!make_q8_plan(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx, true, &q)) return 0;
+  return p.ws_bytes > q.ws_bytes ? p.ws_bytes : q.ws_bytes;
 }
 
 tq_status tq_sdpa_q8(const void* q, tq_dtype q_dtype, int32_t batch, int32_t num_q_heads,

@@ -32,16 +32,22 @@ struct Q8ReadArgs {
   const int32_t *pos, *n_valid;
 };
 
+// The kernel of an attention call, and what a CTA of the tensor-memory one holds
+// (q8_tc.cu).
+enum Q8Mode : int { kQ8Warps, kQ8TwoRows, kQ8TwoStreams, kQ8OneStream };
+
 // How one attention call is split: rows of a kv head (query tokens x query
 // heads per kv head) in tiles, the context in chunks.
 struct Q8Plan {
   int row_tile;     // rows of one work item
   int tiles;        // ceil(n * G / row_tile)
   int chunk;        // context tokens of one work item
-  int n_chunks;     // ceil(max_ctx / chunk); 1 = items write the output themselves
+  int n_chunks;     // ceil(max_ctx / chunk)
+  int parts;        // partial results of one work item
+  int n_parts;      // n_chunks * parts; 1 = items write the output themselves
   int part_stride;  // floats of one partial: d + 4
   size_t header_bytes, ws_bytes;
-  int tensor_memory;  // the tcgen05 kernel serves the call
+  Q8Mode mode;
 };
 
 struct Q8AttendArgs {
@@ -56,14 +62,17 @@ struct Q8AttendArgs {
   float* lse;  // [B][Hq][n][2] or NULL
   void* workspace;
   Q8Plan plan;
+  int test_starve;
 };
 
 bool q8_head_dim_supported(int d);
-bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, int bf16_out, Q8Plan* plan);
+bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, Q8Plan* plan);
 cudaError_t launch_q8_append(const Q8WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t stream);
 int q8_split_slots(int d, int row_tile);  // work items of the split kernel resident on the GPU
 cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream);
+int q8_tc_tile_tokens(int d);             // tokens of one step of the tensor-memory kernel
+cudaError_t launch_q8_tc(const Q8AttendArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream);
 
 #ifdef __CUDACC__

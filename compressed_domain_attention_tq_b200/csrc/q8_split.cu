@@ -377,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         o.w = fmaf(f, v.w, o.w);
       }
       const int64_t orow = ((int64_t)b * a.Hq + hk * G + (row0 + r) % G) * a.n + i;
-      if (a.plan.n_chunks > 1) {
+      if (a.plan.n_parts > 1) {
         float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + a.plan.header_bytes) +
-                      (orow * a.plan.n_chunks + chunk_id) * a.plan.part_stride;
+                      (orow * a.plan.n_parts + chunk_id) * a.plan.part_stride;
         *reinterpret_cast<float4*>(part + x) = o;
         if (x == 0) *reinterpret_cast<float2*>(part + D) = make_float2(M, L);
         continue;
@@ -414,10 +414,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs
   const int b = (int)(orow / ((int64_t)a.Hq * a.n)), i = (int)(orow % a.n);
   const Q8Seq seq(a, b);
   if (i >= seq.q_len) return;
-  const int nc = (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk, stride = a.plan.part_stride;
+  const int nc = (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk * a.plan.parts, stride = a.plan.part_stride;
   const float* part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.workspace) +
                                                      a.plan.header_bytes) +
-                      orow * a.plan.n_chunks * stride;
+                      orow * a.plan.n_parts * stride;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float M = -INFINITY, L = 0.0f;  // of this warp's chunks
   float4 o[P];

@@ -303,6 +303,61 @@ def test_merge_of_context_parts_is_the_whole():
     check(out[:, :, None], want, ref, [300, 129], None)
 
 
+LONG = [  # d, block, H, G, n, ctx, q_lens: many token tiles, row tiles with a rest, prompts from position 0
+    (128, 64, 1, 8, 37, [1100, 37, 300], [37, 37, 1]), (128, 16, 1, 1, 300, [300, 911], [300, 257]),
+    (64, 32, 2, 3, 100, [1500, 100], None), (96, 128, 1, 4, 129, [129, 1025], [64, 129]),
+    (256, 64, 1, 6, 45, [45, 700], [45, 33]), (128, 64, 1, 8, 5, [2000, 5, 129, 0], [5, 4, 1, 5]),
+    (64, 16, 1, 16, 3, [1111, 128], None), (96, 16, 2, 8, 4, [777, 130], [3, 4]),
+    (256, 128, 1, 16, 2, [1500, 64], None), (128, 128, 2, 1, 17, [640, 16], [17, 16]),
+]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,block,H,G,n,ctx,q_lens", LONG)
+def test_attend_bf16_over_many_tiles(fmt, d, block, H, G, n, ctx, q_lens):
+    ref, c = build(d, block, H, ctx, fmt, seed=60)
+    q = randn((len(ctx), H * G, n, d), 61, BF16, 1.5)
+    want, want_lse = ref.attend(f64(q), ctx, q_lens, 1 / math.sqrt(d))
+    marks = torch.full((len(ctx), H * G, n, d), 7.0, device="cuda", dtype=BF16)
+    lse = torch.full((len(ctx), H * G, n, 2), 5.0, device="cuda")
+    got = c.attend(q.cuda(), i32(ctx), max(ctx), q_lens=None if q_lens is None else i32(q_lens), out=marks, lse=lse)
+    check(got, want, ref, ctx, q_lens)
+    lse = f64(lse)
+    for b in range(len(ctx)):
+        m = n if q_lens is None else q_lens[b]
+        with np.errstate(divide="ignore"):
+            np.testing.assert_allclose(lse[b, :, :m, 0] + np.log2(lse[b, :, :m, 1]), want_lse[b, :, :m], atol=4e-3)
+        assert np.all(lse[b, :, m:] == 5.0) and torch.all(got[b, :, m:] == 7.0)
+
+
+def test_bf16_outputs_of_fp32_queries():
+    """The workspace asked for by output type serves queries of either type."""
+    ref, c = build(128, 64, 2, [500, 90], "int8")
+    q = randn((2, 8, 30, 128), 62)
+    want, _ = ref.attend(f64(q), [500, 90], None, 0.1)
+    for dtype in (F32, BF16):
+        x = q.to(dtype)
+        if dtype == BF16:
+            want, _ = ref.attend(f64(x), [500, 90], None, 0.1)
+        out = torch.empty(2, 8, 30, 128, device="cuda", dtype=BF16)
+        ws = torch.empty(_lib.sdpa_q8_workspace_bytes(2, 8, 2, 128, 30, 500, BF16), dtype=torch.uint8, device="cuda")
+        check(c.attend(x.cuda(), i32([500, 90]), 500, attn_scale=0.1, out=out, workspace=ws), want, ref, [500, 90], None)
+
+
+def test_a_pipeline_that_starves_ends_with_nan():
+    """The first tile never arrives: the bounded waits run out and the outputs are NaN."""
+    for n, d in ((64, 128), (8, 128), (64, 256)):
+        ref, c = build(d, 64, 1, [300], "int8")
+        q = randn((1, 4, n, d), 63, BF16).cuda()
+        good = c.attend(q, i32([300]), 300)
+        tq.load().tq_set_test_hooks(2)
+        try:
+            assert torch.isnan(c.attend(q, i32([300]), 300)).all()
+        finally:
+            tq.load().tq_set_test_hooks(0)
+        assert torch.equal(c.attend(q, i32([300]), 300), good)
+
+
 # ------------------------------------------------------------------ used together
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
