@@ -14,9 +14,9 @@
 // In each the products of one S run while the softmax of the other does.
 //
 // Warps.  0..3 and 4..7: softmax, a thread per row, so row statistics need no
-// exchange (d = 256: 0..3 only).  8..11: conversion of codes to f16 operands in
+// exchange (d = 256: 0..3 only).  8..15 (K, V): conversion of codes to f16 operands in
 // shared memory, loaded from global memory one tile ahead into registers.
-// 12: issues the products.
+// 16: issues the products.
 //
 // Numbers.  Codes and the queries (bf16, scaled by a power of two per row) are
 // exact in f16, so scores carry fp32's rounding alone.  A weight is
@@ -47,10 +47,18 @@ namespace {
 using namespace q8;
 using namespace tc;
 
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 4, kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;  // (4 for K and 4 for V)
+constexpr int kMmaWarp = kSoftmaxWarps + 2 * kConvertWarps;
+constexpr int kWarps = 20, kThreads = 32 * kWarps;  // five warpgroups
+constexpr int kConvertThreads = 32 * kConvertWarps;
+// registers of a thread by role: 2 x 136 + 2 x 72 + 64 = 5 x 96, what the block is launched with
+constexpr int kSoftmaxRegs = 136, kConvertRegs = 72, kMmaRegs = 64;
+// kCubic of every 8 pairs of exponentials take the cubic on the FMA pipe: 16 a clock and SM
+// would bound the tile (2 x 128 x 128 of them in the 2048 clocks of its products)
+constexpr int kCubic = 2;
 constexpr float kTau = 8.0f, kShift = 7.0f;  // as in q8_split.cu: weights stay below 2^15
-constexpr float kMinRatio = 0x1p-40f;
+constexpr float kTopSum = 32768.0f;  // 2^(kTau + kShift)
+constexpr float kMasked = -3e38f, kMinRatio = 0x1p-40f;
 constexpr int kScaleSlots = 4;
 
 // tokens of a tile, row tiles in shared memory
@@ -63,10 +71,10 @@ struct Layout {
   static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = T * D * 2;
   static constexpr int Q = 0, K = Q + QT * Q_BYTES, V = K + 2 * KV_BYTES;
   static constexpr int CROW = V + 2 * KV_BYTES;             // float [QT * 128]
-  static constexpr int SCALES = CROW + 4 * QT * 128;        // float4 [kScaleSlots][T / 16]
-  static constexpr int BAR = SCALES + 16 * kScaleSlots * (T / 16);
+  static constexpr int SCALES = CROW + 4 * QT * 128;        // float2 [kScaleSlots][T / 16]
+  static constexpr int BAR = SCALES + 8 * kScaleSlots * (T / 16);
   static constexpr int MISC = BAR + 8 * 32;                 // tmem base, abort, ref, warp maxima
-  static constexpr int BYTES = MISC + 16 + 4 * (kMmaWarp + 1);
+  static constexpr int BYTES = MISC + 16 + 4 * kWarps;
   static_assert(BYTES <= 227 * 1024, "shared memory");
   static __host__ __device__ constexpr uint32_t S(int b) { return (uint32_t)(b * T); }
   static __host__ __device__ constexpr uint32_t O(int u) { return (uint32_t)(2 * T + u * D); }
@@ -78,11 +86,11 @@ enum Bar : int {
   kVFull = 4,
   kVEmpty = 6,
   kSFull = 8,    // [2] scores in tensor memory (commit)
-  kPFull = 10,   // [2] weights in tensor memory (4 softmax warps)
-  kPVDone = 12,  // [2] O up to date (commit)
-  kScFull = 14,  // [kScaleSlots] block scales written (one convert warp)
-  kDone = 18,    // every product complete (commit)
-  kBars = 19
+  kPFull = 10,   // [2][2] the halves of the weights in tensor memory (4 softmax warps)
+  kPVDone = 14,  // [2][2] O up to date with that half of a tile (commit)
+  kScFull = 18,  // [kScaleSlots] block scales written (one convert warp)
+  kDone = 22,    // every product complete (commit)
+  kBars = 23
 };
 
 // What one CTA does: rows of one kv head, and tokens [begin, stop) in nt tiles.
@@ -109,35 +117,82 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
                  "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// O of a warp's 32 rows times alpha
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t col, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tld_x16(col + 16 * c, o);
+    wait_ld();
+    asm volatile("" : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]),
+                 "+r"(o[7]), "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]), "+r"(o[13]),
+                 "+r"(o[14]), "+r"(o[15]));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    tst_x16(col + 16 * c, o);
+  }
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // ------------------------------------------------------------------ conversion
 
+// One thread's 16-byte pieces of a tile of codes: piece i is bytes 16 c .. of token t with
+// p = thread + kConvertThreads i, t = (p & 7) + 8 ((p >> 3) / C), c = (p >> 3) % C, C = D / 16
+// (8 neighbouring tokens in 8 lanes: their stores fill the banks).
 template <int D>
-struct Pieces {  // one thread's 16-byte pieces of a tile of codes
-  static constexpr int N = tile_tokens(D) * D / 16 / (32 * kConvertWarps);
+struct Pieces {
+  static constexpr int T = tile_tokens(D), C = D / 16, N = T * C / kConvertThreads;
+  static constexpr bool kEven = (kConvertThreads / 8) % C == 0;  // all pieces have the same c
   uint4 w[N];
-  // piece p: token (p & 7) + 8 (rest / (D/16)), bytes 16 (rest % (D/16)) .., rest = p >> 3
-  static __device__ __forceinline__ int token(int p) { return (p & 7) + 8 * ((p >> 3) / (D / 16)); }
-  static __device__ __forceinline__ int c16(int p) { return (p >> 3) % (D / 16); }
-  // rows behind the last one repeat it: what is multiplied is always cache content
-  __device__ __forceinline__ void load(const uint8_t* codes, int tok0, int stop, int tid) {
+  static __device__ __forceinline__ int token(int p) { return (p & 7) + 8 * ((p >> 3) / C); }
+  static __device__ __forceinline__ int c16(int p) { return (p >> 3) % C; }
+  static __device__ __forceinline__ int piece(int tid, int i) { return tid + kConvertThreads * i; }
+  __device__ __forceinline__ void load_one(int i, const uint8_t* at) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                 : "l"(at));
+  }
+  // rows of the tile behind the first `rows` repeat the last one: what is multiplied is
+  // always cache content
+  __device__ __forceinline__ void load(const uint8_t* tile, int rows, int tid) {
+    if (kEven && rows >= T) {
+      const uint8_t* at = tile + token(tid) * D + 16 * c16(tid);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = tid + 32 * kConvertWarps * i;
-      const uint8_t* at = codes + (int64_t)min(tok0 + token(p), stop - 1) * D + 16 * c16(p);
-      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "l"(at));
+      for (int i = 0; i < N; ++i) load_one(i, at + i * (kConvertThreads / C) * D);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int p = piece(tid, i);
+        load_one(i, tile + min(token(p), rows - 1) * D + 16 * c16(p));
+      }
     }
   }
   template <typename F>
   __device__ __forceinline__ void store(unsigned char* dst, int tid) const {
-    constexpr int T = tile_tokens(D);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int p = tid + 32 * kConvertWarps * i;
-      unsigned char* at = dst + (2 * c16(p) * T + token(p)) * 16;
+      const int p = piece(tid, i);
+      unsigned char* at = kEven ? dst + (2 * c16(tid) * T + token(tid)) * 16 + i * (kConvertThreads / C) * 16
+                                : dst + (2 * c16(p) * T + token(p)) * 16;
       uint4 lo, hi;
       F::cvt_word(w[i].x, lo.x, lo.y);
       F::cvt_word(w[i].y, lo.z, lo.w);
@@ -151,59 +206,53 @@ struct Pieces {  // one thread's 16-byte pieces of a tile of codes
   }
 };
 
+// K and V have converters of their own (one code, so that it stays in the instruction
+// cache), which keeps two tiles in flight.
 template <typename F, int D, int MODE>
 __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& it, unsigned char* smem,
-                                             uint64_t* bar, volatile int* abort, float ref) {
+                                             uint64_t* bar, volatile int* abort, float ref, bool is_v, int tid) {
   using L = Layout<D, MODE>;
-  const int tid = threadIdx.x - 32 * kSoftmaxWarps, lane = tid & 31;
-  const uint8_t* kc = head_codes<D>(a.c.k_codes, a, it.bh);
-  const uint8_t* vc = head_codes<D>(a.c.v_codes, a, it.bh);
+  const int lane = tid & 31;
+  const uint8_t* tile = head_codes<D>(is_v ? a.c.v_codes : a.c.k_codes, a, it.bh) + (int64_t)it.begin * D;
   const float* ksc = a.c.k_scales + (int64_t)it.bh * a.c.n_blocks();
   const float* vsc = a.c.v_scales + (int64_t)it.bh * a.c.n_blocks();
   const int shift = 31 - __clz(a.c.block);
-  // K runs ahead of V by the tiles whose scores are computed before the first P V
-  constexpr int kAhead = MODE == kQ8TwoRows ? 1 : 2;
-  Pieces<D> k, v;
+  const bool first_k = !is_v && tid < 32, scales = first_k && tid < L::T / 16;  // 16 tokens a thread
+  uint64_t* full = bar + (is_v ? kVFull : kKFull);
+  uint64_t* empty = bar + (is_v ? kVEmpty : kKEmpty);
+  unsigned char* operand = smem + (is_v ? L::V : L::K);
+  Pieces<D> x;
   float sk = 0.0f, sv = 0.0f;
-  auto load_scales = [&](int j) {
+  auto load = [&](int j) {
     if (j >= it.nt) return;
-    const int blk = min(it.begin + j * L::T + 16 * tid, it.stop - 1) >> shift;
-    sk = __ldg(ksc + blk);
-    sv = __ldg(vsc + blk);
+    const int tok0 = it.begin + j * L::T;
+    if (scales) {
+      const int blk = min(tok0 + 16 * tid, it.stop - 1) >> shift;
+      sk = __ldg(ksc + blk);
+      sv = __ldg(vsc + blk);
+    }
+    x.load(tile, it.stop - tok0, tid);
+    tile += L::T * D;
   };
-  if (it.nt > 0) {
-    k.load(kc, it.begin, it.stop, tid);
-    v.load(vc, it.begin, it.stop, tid);
-    if (tid < L::T / 16) load_scales(0);
-  }
-  for (int j = 0; j < it.nt + kAhead - 1; ++j) {
-    if (j < it.nt) {
-      const int s = j & 1;
-      if (j >= 2) warp_wait(bar + kKEmpty + s, ((j >> 1) - 1) & 1, abort);
-      if (tid < 32) {
-        // scales of 16 tokens: {s_k, log2(s_v / ref), ref / s_v}.  Slot j - 4 has been
-        // read: the scores of tile j - 2 came after the weights of tile j - 4.
-        if (tid < L::T / 16) {
-          const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
-          reinterpret_cast<float4*>(smem + L::SCALES)[(j & (kScaleSlots - 1)) * (L::T / 16) + tid] =
-              make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
-          load_scales(j + 1);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar + kScFull + (j & (kScaleSlots - 1)));
+  load(0);
+#pragma unroll 1
+  for (int j = 0; j < it.nt; ++j) {
+    const int s = j & 1;
+    if (j >= 2) warp_wait(empty + s, ((j >> 1) - 1) & 1, abort);
+    if (first_k) {
+      // {s_k, log2(s_v / ref)}.  Slot j - 4 has been read: the scores of tile j - 2 came
+      // after the weights of tile j - 4.
+      const int slot = j & (kScaleSlots - 1);
+      if (scales) {
+        const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
+        reinterpret_cast<float2*>(smem + L::SCALES)[slot * (L::T / 16) + tid] = make_float2(sk, log2f(ratio));
       }
-      k.template store<F>(smem + L::K + s * L::KV_BYTES, tid);
-      if (lane == 0 && !(a.test_starve && j == 0)) mbar_arrive(bar + kKFull + s);
-      if (j + 1 < it.nt) k.load(kc, it.begin + (j + 1) * L::T, it.stop, tid);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + kScFull + slot);
     }
-    const int jv = j - (kAhead - 1);
-    if (jv >= 0 && jv < it.nt) {
-      const int s = jv & 1;
-      if (jv >= 2) warp_wait(bar + kVEmpty + s, ((jv >> 1) - 1) & 1, abort);
-      v.template store<F>(smem + L::V + s * L::KV_BYTES, tid);
-      if (lane == 0) mbar_arrive(bar + kVFull + s);
-      if (jv + 1 < it.nt) v.load(vc, it.begin + (jv + 1) * L::T, it.stop, tid);
-    }
+    x.template store<F>(operand + s * L::KV_BYTES, tid);
+    if (lane == 0 && !(a.test_starve && !is_v && j == 0)) mbar_arrive(full + s);
+    load(j + 1);
   }
 }
 
@@ -214,28 +263,34 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
                                          volatile int* abort, uint32_t tbase) {
   using L = Layout<D, MODE>;
   constexpr uint32_t idS = idesc_f16(128, L::T, 0, 0), idO = idesc_f16(128, D, 0, 1);
-  const uint64_t dq = smem_desc(smem_u32(smem + L::Q), 128 * 16, 128);
-  const uint64_t dk = smem_desc(smem_u32(smem + L::K), L::T * 16, 128);
-  const uint64_t dv = smem_desc(smem_u32(smem + L::V), 128, L::T * 16);
+  // descriptors: the upper words are constants, the lower ones add (bytes / 16) offsets
+  constexpr uint64_t q0 = smem_desc(0, 128 * 16, 128), k0 = smem_desc(0, L::T * 16, 128), v0 = smem_desc(0, 128, L::T * 16);
+  const uint32_t at = smem_u32(smem) >> 4;
   // scores of token tile j into S[b], from row tile u of Q
   auto scores = [&](int j, int u, int b) {
     if (!*abort) {
-      const uint64_t q = dq + (uint64_t)((u * L::Q_BYTES) >> 4), k = dk + (uint64_t)(((j & 1) * L::KV_BYTES) >> 4);
+      const uint32_t q = at + ((L::Q + u * L::Q_BYTES) >> 4), k = at + ((L::K + (j & 1) * L::KV_BYTES) >> 4);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
-        mma_ss(tbase + L::S(b), q + (uint64_t)(c * 2 * 128), k + (uint64_t)(c * 2 * L::T), idS, c > 0);
+        mma_ss(tbase + L::S(b), q0 | (q + c * 2 * 128), k0 | (k + c * 2 * L::T), idS, c > 0);
     }
     mma_commit(bar + kSFull + b);
   };
-  // O[u] += P[b] V of token tile j
-  auto values = [&](int j, int u, int b, bool first) {
-    if (!*abort) {
-      const uint64_t v = dv + (uint64_t)(((j & 1) * L::KV_BYTES) >> 4);
+  // O[u] += P[b] V of token tile j; the weights come in two halves, phase by phase
+  auto values = [&](int j, int u, int b, uint32_t phase, bool first) {
+    const uint32_t v = at + ((L::V + (j & 1) * L::KV_BYTES) >> 4);
+    constexpr int H = L::T / 32;  // products of 16 tokens in a half
 #pragma unroll
-      for (int c = 0; c < L::T / 16; ++c)
-        mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * c, v + (uint64_t)(c * 16), idO, c > 0 || !first);
+    for (int h = 0; h < 2; ++h) {
+      mbar_wait(bar + kPFull + 2 * b + h, phase, abort);
+      fence_after();
+      if (!*abort) {
+#pragma unroll
+        for (int c = h * H; c < (h + 1) * H; ++c)
+          mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * c, v0 | (v + c * 16), idO, c > 0 || !first);
+      }
+      mma_commit(bar + kPVDone + 2 * u + h);
     }
-    mma_commit(bar + kPVDone + u);
   };
   auto wait_k = [&](int j) {
     mbar_wait(bar + kKFull + (j & 1), (j >> 1) & 1, abort);
@@ -254,9 +309,7 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
       wait_v(j);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        mbar_wait(bar + kPFull + u, j & 1, abort);
-        fence_after();
-        values(j, u, u, j == 0);
+        values(j, u, u, j & 1, j == 0);
         if (j + 1 < it.nt) {
           if (u == 0) wait_k(j + 1);
           scores(j + 1, u, u);
@@ -274,9 +327,7 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
     for (int j = 0; j < it.nt; ++j) {
       const int b = j & 1;
       wait_v(j);
-      mbar_wait(bar + kPFull + b, (j >> 1) & 1, abort);
-      fence_after();
-      values(j, MODE == kQ8TwoStreams ? b : 0, b, MODE == kQ8TwoStreams ? j < 2 : j == 0);
+      values(j, MODE == kQ8TwoStreams ? b : 0, b, (j >> 1) & 1, MODE == kQ8TwoStreams ? j < 2 : j == 0);
       mma_commit(bar + kVEmpty + b);
       if (j + 2 < it.nt) {
         wait_k(j + 2);
@@ -291,69 +342,91 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
 
 // --------------------------------------------------------------------- softmax
 
-// (max over a tile's scores of one row, in log2 units): MASK where a row may end inside
-template <int T, bool MASK>
-__device__ __forceinline__ float tile_max(uint32_t s_col, const float4* sc, float crow, int left) {
-  float mx = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < T / 32; ++c) {
-    uint32_t r[32];
-    tld_x32(s_col + 32 * c, r);
-    wait_ld();
-    tie32(r);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = sc[2 * c + h].x * crow;
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float x = __uint_as_float(r[16 * h + i]), y = __uint_as_float(r[16 * h + i + 1]);
-        if constexpr (MASK)
-          top = max3(top, 32 * c + 16 * h + i < left ? x : -INFINITY, 32 * c + 16 * h + i + 1 < left ? y : -INFINITY);
-        else
-          top = max3(top, x, y);
-      }
-      // a masked row's -inf is kept from meeting a scale of 0
-      mx = fmaxf(mx, MASK && top == -INFINITY ? top : top * f);
-    }
-  }
-  return mx;
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by the adder:
+// 1.5 2^23 + x), 2^f by the cubic that minimises the relative error on |f| <= 1/2 (7.5e-5,
+// by exchange; a weight is rounded to 2^-11 anyway), n added to the exponent.  Arguments
+// below -126 count as -126.
+__device__ __forceinline__ float2 ex2_cubic(float2 x) {
+  constexpr float kMagic = 12582912.0f, c0 = 0.99992806f, c1 = 0.69326097f, c2 = 0.24261113f, c3 = 0.05517167f;
+  x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
+  const float2 t = add2(x, make_float2(kMagic, kMagic));
+  const float2 f = fma2(add2(t, make_float2(-kMagic, -kMagic)), make_float2(-1.0f, -1.0f), x);
+  float2 p = fma2(f, make_float2(c3, c3), make_float2(c2, c2));
+  p = fma2(p, f, make_float2(c1, c1));
+  p = fma2(p, f, make_float2(c0, c0));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// Weights of a tile into tensor memory over its scores; returns their sum.
-template <int T, bool MASK>
-__device__ __forceinline__ float tile_weights(uint32_t s_col, const float4* sc, float crow, float m, int left) {
-  float sum = 0.0f;
+// A half tile of H tokens of one row, in registers, and its factors for the scores of
+// each 16 tokens: {s_k crow, log2(s_v / ref)}.
+template <int H>
+struct Half {
+  uint32_t s[H / 32][32];
+  float f[H / 16], lv[H / 16];
+
+  __device__ __forceinline__ void load(uint32_t col) {
 #pragma unroll
-  for (int c = 0; c < T / 32; ++c) {
-    uint32_t r[32], w[16];
-    tld_x32(s_col + 32 * c, r);
+    for (int c = 0; c < H / 32; ++c) tld_x32(col + 32 * c, s[c]);
     wait_ld();
-    tie32(r);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 k = sc[2 * c + h];
-      const float f = k.x * crow, off = k.y - m;
-      float part[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float p[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaf(__uint_as_float(r[16 * h + i + e]), f, off);
-          if constexpr (MASK)
-            if (32 * c + 16 * h + i + e >= left) x = -INFINITY;
-          p[e] = ex2(x);
-          part[e] += p[e];
-        }
-        w[8 * h + i / 2] = f16x2(p[0], p[1]);
-      }
-      sum = fmaf(part[0] + part[1], k.z, sum);
-    }
-    tst_x16(s_col + 16 * c, w);
+    for (int c = 0; c < H / 32; ++c) tie32(s[c]);
   }
-  return sum;
-}
+  __device__ __forceinline__ float at(int i) const { return __uint_as_float(s[i / 32][i % 32]); }
+
+  // The row sees only the first `left` tokens.  A factor of 0 (a block of zeros, whose
+  // scores are 0 with any factor) must not let the others through.
+  __device__ __forceinline__ void mask(int left) {
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      if (i >= left) s[i / 32][i % 32] = __float_as_uint(kMasked);
+#pragma unroll
+    for (int g = 0; g < H / 16; ++g) f[g] = fmaxf(f[g], 1e-30f);
+  }
+
+  // the largest score in log2 units
+  __device__ __forceinline__ float max() const {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < H / 16; ++g) {
+      float top = at(16 * g);
+#pragma unroll
+      for (int i = 16 * g + 1; i < 16 * g + 16; ++i) top = fmaxf(top, at(i));
+      mx = fmaxf(mx, top * f[g]);
+    }
+    return mx;
+  }
+
+  // The weights 2^(x + lv - m), into tensor memory over scores already read.  Returns their
+  // sum without the factors 2^lv; top is the largest sum of 16 with them.
+  __device__ __forceinline__ float weights(uint32_t col, float m, float& top) const {
+    float l = 0.0f;
+    top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < H / 32; ++c) {
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int g = 2 * c + e;
+        const float2 f2 = make_float2(f[g], f[g]), off = make_float2(lv[g] - m, lv[g] - m);
+        float2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fma2(make_float2(at(16 * g + 2 * i), at(16 * g + 2 * i + 1)), f2, off);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = i * kCubic / 8 != (i + 1) * kCubic / 8 ? ex2_cubic(x[i]) : make_float2(ex2(x[i].x), ex2(x[i].y));
+        const float2 s2 = add2(add2(add2(x[0], x[1]), add2(x[2], x[3])), add2(add2(x[4], x[5]), add2(x[6], x[7])));
+        const float sum = s2.x + s2.y;
+        top = fmaxf(top, sum);
+        l = fmaf(sum, ex2(-lv[g]), l);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[8 * e + i] = f16x2(x[i].x, x[i].y);
+      }
+      tst_x16(col + 16 * c, w);
+    }
+    return l;
+  }
+};
 
 template <typename F, int D, int MODE>
 __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& it, const Q8Seq& seq,
@@ -380,49 +453,59 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
     const int phase = MODE == kQ8TwoRows ? j : (j >> 1);
     const uint32_t s_col = tbase + lanes + L::S(sb);
     warp_wait(bar + kScFull + (j & (kScaleSlots - 1)), (j / kScaleSlots) & 1, abort);
+    const float2* sc = reinterpret_cast<const float2*>(smem + L::SCALES) + (j & (kScaleSlots - 1)) * (T / 16);
     warp_wait(bar + kSFull + sb, phase & 1, abort);
     fence_after();
-    if (warp_live) {
-      const float4* sc = reinterpret_cast<const float4*>(smem + L::SCALES) + (j & (kScaleSlots - 1)) * (T / 16);
-      const int tok0 = it.begin + j * T;
-      const bool mask = tok0 + T > min(open, it.stop);
-      const int left = min(limit, it.stop) - tok0;  // tokens of this tile that the row sees
-      const float mx = mask ? tile_max<T, true>(s_col, sc, crow, left) : tile_max<T, false>(s_col, sc, crow, left);
-      if (__any_sync(0xffffffffu, mx > m + (kTau + kShift))) {
-        const float mn = fmaxf(m, mx - kShift);  // m is held 2^kShift low
-        const float alpha = mn == m ? 1.0f : exp2f(m - mn);
-        m = mn;
-        l *= alpha;
-        if (n > 0) {
-          warp_wait(bar + kPVDone + ou, (n - 1) & 1, abort);
-          fence_after();
+    // Each half is a step of the online softmax of its own: its product starts while the
+    // other half's weights are computed, and 64 scores fit in registers.  The weights are
+    // computed with the reference as it is; if 16 of them sum to more than 2^(kTau + kShift)
+    // (f16 would overflow soon) it is moved and they are computed again, so that no maximum
+    // has to be taken otherwise.
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (warp_live) {
+        constexpr int H = T / 2;
+        Half<H> x;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tld_x16(tbase + lanes + L::O(ou) + 16 * c, o);
-            wait_ld();
-            asm volatile("" : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]),
-                         "+r"(o[7]), "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]),
-                         "+r"(o[13]), "+r"(o[14]), "+r"(o[15]));
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tst_x16(tbase + lanes + L::O(ou) + 16 * c, o);
-          }
+        for (int g = 0; g < H / 16; ++g) {
+          const float2 k = sc[h * (H / 16) + g];
+          x.f[g] = k.x * crow;
+          x.lv[g] = k.y;
         }
+        const int tok0 = it.begin + j * T + h * H;
+        const int left = min(limit, it.stop) - tok0;  // tokens of this half that the row sees
+        x.load(s_col + h * H);
+        if (tok0 + H > min(open, it.stop)) x.mask(left);
+        const uint32_t p_col = s_col + h * (H / 2);
+        float top, sum = x.weights(p_col, m == -INFINITY ? 0.0f : m, top);
+        const bool move = top > kTopSum || m == -INFINITY;
+        if (__any_sync(0xffffffffu, move)) {
+          const float mn = move && left > 0 ? fmaxf(m, x.max() - kShift) : m;  // m is held 2^kShift low
+          const float alpha = mn == m ? 1.0f : exp2f(m - mn);
+          m = mn;
+          l *= alpha;
+          if (n + h > 0) {  // once O is up to date
+            if (n > 0) warp_wait(bar + kPVDone + 2 * ou + 1, (n - 1) & 1, abort);
+            if (h > 0) warp_wait(bar + kPVDone + 2 * ou, n & 1, abort);
+            fence_after();
+            rescale<D>(tbase + lanes + L::O(ou), alpha);
+          }
+          wait_st();
+          sum = x.weights(p_col, m == -INFINITY ? 0.0f : m, top);
+        }
+        l += sum;
+        wait_st();
+        fence_before();
+        __syncwarp();
       }
-      const float mm = m == -INFINITY ? 0.0f : m;
-      l += mask ? tile_weights<T, true>(s_col, sc, crow, mm, left)
-                : tile_weights<T, false>(s_col, sc, crow, mm, left);
-      wait_st();
+      if (lane == 0) mbar_arrive(bar + kPFull + 2 * sb + h);
     }
-    fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar + kPFull + sb);
   }
-  if (n > 0) warp_wait(bar + kPVDone + ou, (n - 1) & 1, abort);
+  if (it.nt > 0) warp_wait(bar + kDone, 0, abort);
   fence_after();
   if (!warp_live) return;
-  const bool none = n == 0 || (m == -INFINITY && l == 0.0f);
+  const bool none = n == 0 || (m == -INFINITY && l < 1e-20f);  // (masked weights of the cubic are 2^-126)
+  if (none) l = 0.0f;
   const int64_t orow = ((int64_t)it.b * a.Hq + it.hk * it.G + r % it.G) * a.n + i;
   const bool split = a.plan.n_parts > 1;
   if (*abort) l = __int_as_float(0x7fc00000);
@@ -506,6 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
       mbar_init(bar + kVFull + i, kConvertWarps);
       mbar_init(bar + kVEmpty + i, 1);
       mbar_init(bar + kSFull + i, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar + kPFull + i, 4);
       mbar_init(bar + kPVDone + i, 1);
     }
@@ -533,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   float* crow = reinterpret_cast<float*>(smem + L::CROW);
   constexpr int W = (D / 4 + 31) / 32;  // words of four elements per lane
 #pragma unroll 2
-  for (int r = warp; r < L::QT * 128; r += kMmaWarp + 1) {
+  for (int r = warp; r < L::QT * 128; r += kWarps) {
     const int row = it.row0 + r, i = row / it.G;
     const bool live = row < it.rows && i < seq.q_len;
     const uint16_t* q = static_cast<const uint16_t*>(a.q) +
@@ -573,15 +659,20 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   const uint32_t tbase = static_cast<uint32_t>(misc[0]);
   float ref = 0.0f;
 #pragma unroll
-  for (int w = 0; w <= kMmaWarp; ++w) ref = fmaxf(ref, warp_max[w]);
+  for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, warp_max[w]);
 
   if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     if (MODE != kQ8OneStream || warp < 4)
       softmax_role<F, D, MODE>(a, it, seq, smem, bar, abort, tbase, ref);
   } else if (warp < kMmaWarp) {
-    convert_role<F, D, MODE>(a, it, smem, bar, abort, ref);
-  } else if (it.nt > 0 && lane == 0) {
-    mma_role<D, MODE>(it, smem, bar, abort, tbase);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+    const int tid = threadIdx.x - 32 * kSoftmaxWarps;
+    const bool is_v = tid >= kConvertThreads;
+    convert_role<F, D, MODE>(a, it, smem, bar, abort, ref, is_v, is_v ? tid - kConvertThreads : tid);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kMmaWarp && it.nt > 0 && lane == 0) mma_role<D, MODE>(it, smem, bar, abort, tbase);
   }
   __syncwarp();
   fence_before();
