@@ -54,12 +54,12 @@ tq_status check_cache(const void* k_codes, const float* k_scales, const void* v_
 
 namespace {
 
-// Chunks of the context for one call: the count that minimises
+// Chunks of the context for `units` units: the count that minimises
 // (waves of work items over the resident CTAs) x (tokens of one item + a fixed
-// cost per item, in tokens).  A call whose rows alone fill the GPU is not split.
+// cost per item, in tokens).
 void split_context(int64_t units, int64_t slots, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
   int64_t best = ceil_div(max_ctx, step) * step, best_cost = -1;
-  for (int64_t k = 1; k <= ceil_div(max_ctx, step) && k <= 1024; ++k) {
+  for (int64_t k = 1; units > 0 && k <= ceil_div(max_ctx, step) && k <= 1024; ++k) {
     const int64_t chunk = ceil_div(ceil_div(max_ctx, k), step) * step;
     const int64_t items = units * ceil_div(max_ctx, chunk);
     const int64_t cost = ceil_div(items, slots) * (chunk + item_cost);
@@ -86,7 +86,7 @@ bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, 
     p->parts = p->mode == kQ8TwoStreams ? 2 : 1;
     slots = kSmCount;
     step = p->parts * q8_tc_tile_tokens(d);
-    item_cost = 1024;
+    item_cost = 512;
   } else {
     p->mode = kQ8Warps;
     p->row_tile = rows <= 8 ? 8 : 16;
@@ -97,14 +97,16 @@ bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, 
   }
   p->tiles = (int)ceil_div(rows, p->row_tile);
   const int64_t units = (int64_t)B * Hkv * p->tiles;
-  split_context(units, slots, max_ctx, step, item_cost, p);
+  if (units > INT32_MAX) return false;
+  p->units = (int)units;
+  p->whole = p->parts > 1 ? 0 : (int)(units / slots * slots);
+  split_context(units - p->whole, slots, max_ctx, step, item_cost, p);
   p->n_parts = p->n_chunks * p->parts;
+  if (p->n_parts == 1) p->whole = (int)units;
   p->part_stride = d + 4;
   p->header_bytes = (size_t)ceil_div(4LL * B, 256) * 256;
-  p->ws_bytes = p->header_bytes;
-  if (p->n_parts > 1)
-    p->ws_bytes += sizeof(float) * (size_t)B * Hq * n * p->n_parts * p->part_stride;
-  return units * p->n_chunks <= INT32_MAX;
+  p->ws_bytes = p->header_bytes + sizeof(float) * (size_t)p->split_rows() * p->n_parts * p->part_stride;
+  return p->items() <= INT32_MAX && p->split_rows() <= INT32_MAX;
 }
 
 namespace {
@@ -145,7 +147,7 @@ tq_status attend(const void* q, tq_dtype q_dtype, int32_t num_q_heads, int32_t n
   a.test_starve = (hooks & TQ_TEST_HOOK_STARVE_PIPELINE) != 0;
   cudaError_t e = append ? launch_q8_append(*append, stream) : cudaSuccess;
   if (e == cudaSuccess) e = a.plan.mode == kQ8Warps ? launch_q8_split(a, stream) : launch_q8_tc(a, stream);
-  if (e == cudaSuccess && a.plan.n_parts > 1) e = launch_q8_merge(a, stream);
+  if (e == cudaSuccess && a.plan.whole < a.plan.units) e = launch_q8_merge(a, stream);
   return status_of(e, where);
 }
 

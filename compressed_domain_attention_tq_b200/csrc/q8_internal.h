@@ -36,18 +36,24 @@ struct Q8ReadArgs {
 // (q8_tc.cu).
 enum Q8Mode : int { kQ8Warps, kQ8TwoRows, kQ8TwoStreams, kQ8OneStream };
 
-// How one attention call is split: rows of a kv head (query tokens x query
-// heads per kv head) in tiles, the context in chunks.
+// How one attention call is split.  A unit is one tile of rows (query tokens x query heads
+// of a kv head) of one kv head; units are numbered from the last tile, which attends most.
+// The first `whole` ones are one work item each and write their outputs; the others, too few
+// to fill the GPU once more, are split into chunks of the context, whose partial results
+// the merge joins.
 struct Q8Plan {
   int row_tile;     // rows of one work item
   int tiles;        // ceil(n * G / row_tile)
-  int chunk;        // context tokens of one work item
+  int whole, units;
+  int chunk;        // context tokens of one work item of a split unit
   int n_chunks;     // ceil(max_ctx / chunk)
   int parts;        // partial results of one work item
-  int n_parts;      // n_chunks * parts; 1 = items write the output themselves
+  int n_parts;      // n_chunks * parts: of a row of a split unit
   int part_stride;  // floats of one partial: d + 4
   size_t header_bytes, ws_bytes;
   Q8Mode mode;
+  int64_t items() const { return whole + (int64_t)(units - whole) * n_chunks; }
+  int64_t split_rows() const { return (int64_t)(units - whole) * row_tile; }
 };
 
 struct Q8AttendArgs {
@@ -76,6 +82,40 @@ cudaError_t launch_q8_tc(const Q8AttendArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream);
 
 #ifdef __CUDACC__
+// The unit, and the chunk of it, that work item `id` is.
+struct Q8Item {
+  int unit, chunk_id, tile, bh, b, hk, G, rows, row0;
+  bool split;
+  __device__ __forceinline__ Q8Item(const Q8AttendArgs& a, int id) {
+    const int e = id - a.plan.whole;
+    split = e >= 0;
+    place(a, split ? a.plan.whole + e / a.plan.n_chunks : id);
+    chunk_id = split ? e % a.plan.n_chunks : 0;
+  }
+  __device__ __forceinline__ Q8Item() {}
+  __device__ __forceinline__ void place(const Q8AttendArgs& a, int u) {
+    unit = u;
+    const int heads = a.c.B * a.c.Hkv;
+    tile = a.plan.tiles - 1 - u / heads;
+    bh = u % heads;
+    b = bh / a.c.Hkv;
+    hk = bh % a.c.Hkv;
+    G = a.Hq / a.c.Hkv;
+    rows = a.n * G;
+    row0 = tile * a.plan.row_tile;
+  }
+  // query token and output row of the tile's row r
+  __device__ __forceinline__ int token(int r) const { return (row0 + r) / G; }
+  __device__ __forceinline__ int64_t out_row(const Q8AttendArgs& a, int r) const {
+    return ((int64_t)b * a.Hq + hk * G + (row0 + r) % G) * a.n + token(r);
+  }
+  // partial p of row r
+  __device__ __forceinline__ float* part(const Q8AttendArgs& a, int r, int p) const {
+    return reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + a.plan.header_bytes) +
+           (((int64_t)(unit - a.plan.whole) * a.plan.row_tile + r) * a.plan.n_parts + p) * a.plan.part_stride;
+  }
+};
+
 // The part of a sequence that its query rows see: query i sits at position
 // ctx - q_len + i and attends the rows up to it.
 struct Q8Seq {

@@ -132,23 +132,20 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   constexpr int KW = D / 16, VW = D / 32, MT = D / 16;
   const Q8Cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int chunk_id = blockIdx.x % a.plan.n_chunks;
-  const unsigned unit = blockIdx.x / a.plan.n_chunks;
-  const int tile = unit % a.plan.tiles;
-  const int bh = unit / a.plan.tiles, b = bh / c.Hkv, hk = bh % c.Hkv;
-  const int G = a.Hq / c.Hkv, rows = a.n * G, row0 = tile * 8 * NT;
+  const Q8Item it(a, blockIdx.x);
+  const int bh = it.bh, b = it.b, hk = it.hk, G = it.G, rows = it.rows, row0 = it.row0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // a decode step's append comes first
   const Q8Seq seq(a, b);
-  if (chunk_id == 0 && tile == 0 && hk == 0 && threadIdx.x == 0)
+  if (it.chunk_id == 0 && it.tile == 0 && hk == 0 && threadIdx.x == 0)
     static_cast<int32_t*>(a.workspace)[b] = seq.bad;
 
   const int last_i = min(rows - 1, row0 + 8 * NT - 1) / G;  // the tile's last and first query token
   const int first_i = row0 / G;
   const int q_last = min(last_i, seq.q_len - 1);
   const int stop_all = q_last < first_i ? 0 : seq.limit(q_last);  // rows any of the tile's queries sees
-  const int begin = chunk_id * a.plan.chunk;
-  const int stop = min(stop_all, begin + a.plan.chunk);
-  if (begin >= stop && (chunk_id > 0 || a.plan.n_chunks > 1)) return;
+  const int begin = it.chunk_id * a.plan.chunk;
+  const int stop = it.split ? min(stop_all, begin + a.plan.chunk) : stop_all;
+  if (begin >= stop && it.split) return;
 
   // -- query fragments, each row scaled so that its largest element is in [2^13, 2^14)
   for (int r = warp; r < 8 * NT; r += kWarps) {
@@ -376,14 +373,13 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
       }
-      const int64_t orow = ((int64_t)b * a.Hq + hk * G + (row0 + r) % G) * a.n + i;
-      if (a.plan.n_parts > 1) {
-        float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + a.plan.header_bytes) +
-                      (orow * a.plan.n_parts + chunk_id) * a.plan.part_stride;
+      if (it.split) {
+        float* part = it.part(a, r, it.chunk_id);
         *reinterpret_cast<float4*>(part + x) = o;
         if (x == 0) *reinterpret_cast<float2*>(part + D) = make_float2(M, L);
         continue;
       }
+      const int64_t orow = it.out_row(a, r);
       const bool none = M == -INFINITY && L == 0.0f;  // no row seen
       const float inv = none ? 0.0f : 1.0f / L;
       o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -397,40 +393,40 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   }
 }
 
-// Joins the chunks of each query row: with M = max m_c, o = sum 2^(m_c - M)
-// acc_c / sum 2^(m_c - M) l_c.  One CTA per row, warp w takes the chunks w,
-// w + 8, ... with a lane on every fourth output element, so a row of up to 64
-// chunks is eight independent loads deep; the eight sums meet in shared memory.
-// The launch is the split kernel's programmatic dependent, so its start overlaps
-// the split's tail.
+// Joins the partials of each row of the split units: with M = max m_c, o = sum
+// 2^(m_c - M) acc_c / sum 2^(m_c - M) l_c.  W warps take a row, warp w its partials w,
+// w + W, ... with a lane on every fourth output element; their sums meet in shared memory.
+// Eight warps make a row of up to 32 partials four independent loads deep (decode: few rows);
+// with up to eight partials a row a warp of its own takes it (many rows).  The launch is the
+// first kernel's programmatic dependent, so its start overlaps that one's tail.
 constexpr int kMergeWarps = 8;
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs a) {
   constexpr int P = (D + 127) / 128;  // pieces of 128 elements
   __shared__ float4 sums[kMergeWarps][P][32];
   __shared__ float2 state[kMergeWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t orow = blockIdx.x;
-  const int b = (int)(orow / ((int64_t)a.Hq * a.n)), i = (int)(orow % a.n);
-  const Q8Seq seq(a, b);
-  if (i >= seq.q_len) return;
-  const int nc = (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk * a.plan.parts, stride = a.plan.part_stride;
-  const float* part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.workspace) +
-                                                     a.plan.header_bytes) +
-                      orow * a.plan.n_parts * stride;
+  const int lane = threadIdx.x & 31, team = (threadIdx.x >> 5) / W, warp = (threadIdx.x >> 5) % W;
+  const int64_t id = (int64_t)blockIdx.x * (kMergeWarps / W) + team;
+  Q8Item it;
+  it.place(a, a.plan.whole + (int)min(id / a.plan.row_tile, (int64_t)(a.plan.units - a.plan.whole - 1)));
+  const int r = (int)(id % a.plan.row_tile), i = it.token(r);
+  const Q8Seq seq(a, it.b);
+  const bool live = id < (int64_t)(a.plan.units - a.plan.whole) * a.plan.row_tile && it.row0 + r < it.rows && i < seq.q_len;
+  const int nc = live ? (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk * a.plan.parts : 0, stride = a.plan.part_stride;
+  const float* part = it.part(a, r, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float M = -INFINITY, L = 0.0f;  // of this warp's chunks
   float4 o[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) o[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   constexpr int U = 4;
-  for (int k0 = warp; k0 < nc; k0 += U * kMergeWarps) {
+  for (int k0 = warp; k0 < nc; k0 += U * W) {
     float2 ml[U];
     float4 v[U][P];
     float top = M;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * kMergeWarps;
+      const int k = k0 + u * W;
       const float* pk = part + (int64_t)k * stride;
       ml[u] = k < nc ? *reinterpret_cast<const float2*>(pk + D) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
@@ -460,35 +456,43 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs
     }
   }
 #pragma unroll
-  for (int p = 0; p < P; ++p) sums[warp][p][lane] = o[p];
-  if (lane == 0) state[warp] = make_float2(M, L);
-  __syncthreads();
-  if (threadIdx.x >= D / 4) return;  // a thread per four output elements
+  for (int p = 0; p < P; ++p) sums[team * W + warp][p][lane] = o[p];
+  if (lane == 0) state[team * W + warp] = make_float2(M, L);
+  if constexpr (W > 1)
+    __syncthreads();
+  else
+    __syncwarp();
+  // the team's threads, one per four output elements
+  const int at = threadIdx.x - 32 * W * team;
+  if (!live) return;
   M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, state[w].x);
+  for (int w = 0; w < W; ++w) M = fmaxf(M, state[team * W + w].x);
   const float base = M == -INFINITY ? 0.0f : M;
-  L = 0.0f;
-  float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int64_t orow = it.out_row(a, r);
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = exp2f(state[w].x - base);
-    const float4 v = sums[w][threadIdx.x >> 5][lane];
-    L = fmaf(f, state[w].y, L);
-    r.x = fmaf(f, v.x, r.x);
-    r.y = fmaf(f, v.y, r.y);
-    r.z = fmaf(f, v.z, r.z);
-    r.w = fmaf(f, v.w, r.w);
+  for (int x4 = at; x4 < D / 4; x4 += 32 * W) {
+    L = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = exp2f(state[team * W + w].x - base);
+      const float4 s = sums[team * W + w][x4 >> 5][x4 & 31];
+      L = fmaf(f, state[team * W + w].y, L);
+      v.x = fmaf(f, s.x, v.x);
+      v.y = fmaf(f, s.y, v.y);
+      v.z = fmaf(f, s.z, v.z);
+      v.w = fmaf(f, s.w, v.w);
+    }
+    const float inv = nc == 0 ? 0.0f : 1.0f / L;
+    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    if (a.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * x4) =
+          make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + 4 * x4) = v;
+    if (a.lse != nullptr && x4 == 0) *reinterpret_cast<float2*>(a.lse + orow * 2) = make_float2(M, L);
   }
-  const float inv = nc == 0 ? 0.0f : 1.0f / L;
-  r = make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
-  const int x = 4 * threadIdx.x;
-  if (a.out_bf16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + x) =
-        make_uint2(bf16x2(r.x, r.y), bf16x2(r.z, r.w));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) = r;
-  if (a.lse != nullptr && x == 0) *reinterpret_cast<float2*>(a.lse + orow * 2) = make_float2(M, L);
 }
 
 template <typename F, int D, int NT>
@@ -497,9 +501,8 @@ cudaError_t launch_one(const Q8AttendArgs& a, cudaStream_t stream) {
   constexpr int bytes = sizeof(Smem<D, NT>);
   const cudaError_t e = ensure_smem_limit(split_kernel<F, D, NT>, bytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = (int64_t)a.c.B * a.c.Hkv * a.plan.tiles * a.plan.n_chunks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)a.plan.items());
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
@@ -525,9 +528,12 @@ cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream) {
   return a.c.e4m3 ? launch_format<E4m3>(a, stream) : launch_format<Int8>(a, stream);
 }
 
-cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
+template <int D>
+static cudaError_t merge_rows(const Q8AttendArgs& a, cudaStream_t stream) {
+  const bool few = a.plan.n_parts <= 8;
+  const int per_cta = few ? kMergeWarps : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.c.B * a.Hq * a.n));
+  cfg.gridDim = dim3((unsigned)((a.plan.split_rows() + per_cta - 1) / per_cta));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -535,11 +541,16 @@ cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, 1>, a)
+             : cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, kMergeWarps>, a);
+}
+
+cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
   switch (a.c.d) {
-    case 64: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<64>, a);
-    case 96: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<96>, a);
-    case 128: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<128>, a);
-    default: return cudaLaunchKernelEx(&cfg, merge_q8_kernel<256>, a);
+    case 64: return merge_rows<64>(a, stream);
+    case 96: return merge_rows<96>(a, stream);
+    case 128: return merge_rows<128>(a, stream);
+    default: return merge_rows<256>(a, stream);
   }
 }
 

@@ -21,7 +21,7 @@
 // Numbers.  Codes and the queries (bf16, scaled by a power of two per row) are
 // exact in f16, so scores carry fp32's rounding alone.  A weight is
 // 2^(x - m) s_v / ref with x = S s_k scale log2(e), m the row's reference (moved
-// only when a score exceeds it by 2^8) and ref the item's largest V scale; it is
+// only when weights get large) and ref the item's largest V scale; it is
 // rounded to f16's 11 bits, as the bf16 output keeps 8.  The ratio enters as
 // its logarithm in the exponent, so it costs nothing; it is floored at 2^-40:
 // a block whose scale is that far below ref then counts with at most
@@ -55,9 +55,10 @@ constexpr int kConvertThreads = 32 * kConvertWarps;
 constexpr int kSoftmaxRegs = 136, kConvertRegs = 72, kMmaRegs = 64;
 // kCubic of every 8 pairs of exponentials take the cubic on the FMA pipe: 16 a clock and SM
 // would bound the tile (2 x 128 x 128 of them in the 2048 clocks of its products)
-constexpr int kCubic = 2;
-constexpr float kTau = 8.0f, kShift = 7.0f;  // as in q8_split.cu: weights stay below 2^15
-constexpr float kTopSum = 32768.0f;  // 2^(kTau + kShift)
+constexpr int kCubic = 1;
+// as in q8_split.cu the reference is held 2^kShift below the maximum it was taken from, and
+// moves when weights reach 2^15
+constexpr float kShift = 7.0f, kTopSum = 32768.0f;
 constexpr float kMasked = -3e38f, kMinRatio = 0x1p-40f;
 constexpr int kScaleSlots = 4;
 
@@ -93,9 +94,10 @@ enum Bar : int {
   kBars = 23
 };
 
-// What one CTA does: rows of one kv head, and tokens [begin, stop) in nt tiles.
-struct Item {
-  int chunk_id, tile, b, hk, bh, G, rows, row0, begin, stop, nt;
+// What one CTA does: a work item's rows, and tokens [begin, stop) in nt tiles.
+struct Item : Q8Item {
+  int begin, stop, nt;
+  __device__ __forceinline__ Item(const Q8AttendArgs& a, int id) : Q8Item(a, id) {}
 };
 
 template <int D>
@@ -107,6 +109,12 @@ __device__ __forceinline__ const uint8_t* head_codes(const uint8_t* codes, const
 __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   mbar_wait(bar, parity, abort);
   __syncwarp();
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Pins registers written by tcgen05.ld behind the wait before this.
@@ -150,8 +158,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // ------------------------------------------------------------------ conversion
 
@@ -258,6 +264,8 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
 
 // -------------------------------------------------------------------- products
 
+// The whole warp runs this, so that addresses and descriptors stay in uniform registers;
+// one elected thread issues.
 template <int D, int MODE>
 __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, uint64_t* bar,
                                          volatile int* abort, uint32_t tbase) {
@@ -266,15 +274,19 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
   // descriptors: the upper words are constants, the lower ones add (bytes / 16) offsets
   constexpr uint64_t q0 = smem_desc(0, 128 * 16, 128), k0 = smem_desc(0, L::T * 16, 128), v0 = smem_desc(0, 128, L::T * 16);
   const uint32_t at = smem_u32(smem) >> 4;
+  const bool leader = elect_one();
+  auto commit = [&](int b) {
+    if (leader) mma_commit(bar + b);
+  };
   // scores of token tile j into S[b], from row tile u of Q
   auto scores = [&](int j, int u, int b) {
-    if (!*abort) {
-      const uint32_t q = at + ((L::Q + u * L::Q_BYTES) >> 4), k = at + ((L::K + (j & 1) * L::KV_BYTES) >> 4);
+    const uint32_t q = at + ((L::Q + u * L::Q_BYTES) >> 4), k = at + ((L::K + (j & 1) * L::KV_BYTES) >> 4);
+    if (leader && !*abort) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
         mma_ss(tbase + L::S(b), q0 | (q + c * 2 * 128), k0 | (k + c * 2 * L::T), idS, c > 0);
     }
-    mma_commit(bar + kSFull + b);
+    commit(kSFull + b);
   };
   // O[u] += P[b] V of token tile j; the weights come in two halves, phase by phase
   auto values = [&](int j, int u, int b, uint32_t phase, bool first) {
@@ -282,29 +294,30 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
     constexpr int H = L::T / 32;  // products of 16 tokens in a half
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      mbar_wait(bar + kPFull + 2 * b + h, phase, abort);
+      warp_wait(bar + kPFull + 2 * b + h, phase, abort);
       fence_after();
-      if (!*abort) {
+      if (leader && !*abort) {
 #pragma unroll
         for (int c = h * H; c < (h + 1) * H; ++c)
           mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * c, v0 | (v + c * 16), idO, c > 0 || !first);
       }
-      mma_commit(bar + kPVDone + 2 * u + h);
+      commit(kPVDone + 2 * u + h);
     }
   };
   auto wait_k = [&](int j) {
-    mbar_wait(bar + kKFull + (j & 1), (j >> 1) & 1, abort);
+    warp_wait(bar + kKFull + (j & 1), (j >> 1) & 1, abort);
     fence_after();
   };
   auto wait_v = [&](int j) {
-    mbar_wait(bar + kVFull + (j & 1), (j >> 1) & 1, abort);
+    warp_wait(bar + kVFull + (j & 1), (j >> 1) & 1, abort);
     fence_after();
   };
   if constexpr (MODE == kQ8TwoRows) {
     wait_k(0);
     scores(0, 0, 0);
     scores(0, 1, 1);
-    mma_commit(bar + kKEmpty);
+    commit(kKEmpty);
+#pragma unroll 1
     for (int j = 0; j < it.nt; ++j) {
       wait_v(j);
 #pragma unroll
@@ -315,29 +328,30 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
           scores(j + 1, u, u);
         }
       }
-      mma_commit(bar + kVEmpty + (j & 1));
-      if (j + 1 < it.nt) mma_commit(bar + kKEmpty + ((j + 1) & 1));
+      commit(kVEmpty + (j & 1));
+      if (j + 1 < it.nt) commit(kKEmpty + ((j + 1) & 1));
     }
   } else {
     for (int j = 0; j < 2 && j < it.nt; ++j) {
       wait_k(j);
       scores(j, 0, j);
-      mma_commit(bar + kKEmpty + j);
+      commit(kKEmpty + j);
     }
+#pragma unroll 1
     for (int j = 0; j < it.nt; ++j) {
       const int b = j & 1;
       wait_v(j);
       values(j, MODE == kQ8TwoStreams ? b : 0, b, (j >> 1) & 1, MODE == kQ8TwoStreams ? j < 2 : j == 0);
-      mma_commit(bar + kVEmpty + b);
+      commit(kVEmpty + b);
       if (j + 2 < it.nt) {
         wait_k(j + 2);
         scores(j + 2, 0, b);
-        mma_commit(bar + kKEmpty + b);
+        commit(kKEmpty + b);
       }
     }
   }
-  mma_commit(bar + kDone);
-  mbar_drain(bar + kDone, 0);
+  commit(kDone);
+  if (leader) mbar_drain(bar + kDone, 0);
 }
 
 // --------------------------------------------------------------------- softmax
@@ -458,7 +472,7 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
     fence_after();
     // Each half is a step of the online softmax of its own: its product starts while the
     // other half's weights are computed, and 64 scores fit in registers.  The weights are
-    // computed with the reference as it is; if 16 of them sum to more than 2^(kTau + kShift)
+    // computed with the reference as it is; if 16 of them sum to more than kTopSum
     // (f16 would overflow soon) it is moved and they are computed again, so that no maximum
     // has to be taken otherwise.
 #pragma unroll 1
@@ -506,13 +520,12 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
   if (!warp_live) return;
   const bool none = n == 0 || (m == -INFINITY && l < 1e-20f);  // (masked weights of the cubic are 2^-126)
   if (none) l = 0.0f;
-  const int64_t orow = ((int64_t)it.b * a.Hq + it.hk * it.G + r % it.G) * a.n + i;
-  const bool split = a.plan.n_parts > 1;
+  const int64_t orow = it.out_row(a, local);
+  const bool split = it.split;
   if (*abort) l = __int_as_float(0x7fc00000);
   const float f = none ? 0.0f : split ? ref : ref / l;
   const int part_id = MODE == kQ8TwoStreams ? 2 * it.chunk_id + u : it.chunk_id;
-  float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.workspace) + a.plan.header_bytes) +
-                (orow * a.plan.n_parts + part_id) * a.plan.part_stride;
+  float* part = it.part(a, local, part_id);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
     uint32_t o[32];
@@ -558,17 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   int* misc = reinterpret_cast<int*>(smem + L::MISC);
   volatile int* abort = misc + 1;
   float* warp_max = reinterpret_cast<float*>(misc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Item it;
-  it.chunk_id = blockIdx.x % a.plan.n_chunks;
-  const unsigned unit = blockIdx.x / a.plan.n_chunks;
-  it.tile = a.plan.tiles - 1 - (int)(unit % a.plan.tiles);  // the longest first
-  it.bh = unit / a.plan.tiles;
-  it.b = it.bh / a.c.Hkv;
-  it.hk = it.bh % a.c.Hkv;
-  it.G = a.Hq / a.c.Hkv;
-  it.rows = a.n * it.G;
-  it.row0 = it.tile * a.plan.row_tile;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  Item it(a, blockIdx.x);
   const Q8Seq seq(a, it.b);
   if (it.chunk_id == 0 && it.tile == 0 && it.hk == 0 && threadIdx.x == 0)
     static_cast<int32_t*>(a.workspace)[it.b] = seq.bad;
@@ -576,10 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   const int q_last = min(min(it.rows - 1, it.row0 + a.plan.row_tile - 1) / it.G, seq.q_len - 1);
   const int stop_all = q_last < first_i ? 0 : seq.limit(q_last);
   it.begin = it.chunk_id * a.plan.chunk;
-  it.stop = min(stop_all, it.begin + a.plan.chunk);
+  it.stop = it.split ? min(stop_all, it.begin + a.plan.chunk) : stop_all;
   it.nt = max(0, (it.stop - it.begin + L::T - 1) / L::T);
-  // nothing to do (but a first chunk of no token still writes its rows' zeros)
-  if (q_last < first_i || (it.nt == 0 && it.chunk_id > 0)) return;
+  // nothing to do (rows that see no token get zeros here, or from the merge)
+  if (q_last < first_i || (it.nt == 0 && it.split)) return;
 
   if (threadIdx.x == 0) {
 #pragma unroll
@@ -618,39 +622,49 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   // queries: each row scaled so that its largest element is in [2^13, 2^14)
   float* crow = reinterpret_cast<float*>(smem + L::CROW);
   constexpr int W = (D / 4 + 31) / 32;  // words of four elements per lane
-#pragma unroll 2
-  for (int r = warp; r < L::QT * 128; r += kWarps) {
-    const int row = it.row0 + r, i = row / it.G;
-    const bool live = row < it.rows && i < seq.q_len;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) +
-                        (((int64_t)it.b * a.Hq + it.hk * it.G + row % it.G) * a.n + i) * D;
-    float x[W][4];
-    float big = 0.0f;
+  constexpr int R = 7;                  // rows of a warp whose loads are in flight together
+#pragma unroll 1
+  for (int r0 = warp; r0 < L::QT * 128; r0 += R * kWarps) {
+    uint2 v[R][W];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      uint2 v = make_uint2(0u, 0u);
-      if (live && lane + 32 * w < D / 4) v = *reinterpret_cast<const uint2*>(q + 4 * (lane + 32 * w));
-      x[w][0] = __uint_as_float(v.x << 16);
-      x[w][1] = __uint_as_float(v.x & 0xffff0000u);
-      x[w][2] = __uint_as_float(v.y << 16);
-      x[w][3] = __uint_as_float(v.y & 0xffff0000u);
+    for (int k = 0; k < R; ++k) {
+      const int r = r0 + k * kWarps;
+      const bool live = r < L::QT * 128 && it.row0 + r < it.rows && it.token(r) < seq.q_len;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + it.out_row(a, r) * D;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[w][e]));
+      for (int w = 0; w < W; ++w)
+        v[k][w] = live && lane + 32 * w < D / 4 ? *reinterpret_cast<const uint2*>(q + 4 * (lane + 32 * w))
+                                                : make_uint2(0u, 0u);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-    const int e = big > 0.0f ? max(-100, min(100, 13 - ilogbf(big))) : 0;
-    const float up = pow2i(e);
-    unsigned char* dst = smem + L::Q + (r >> 7) * L::Q_BYTES + (r & 127) * 16;
+    for (int k = 0; k < R; ++k) {
+      const int r = r0 + k * kWarps;
+      if (r >= L::QT * 128) break;
+      float x[W][4], big = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const int word = lane + 32 * w;
-      if (word < D / 4)
-        *reinterpret_cast<uint2*>(dst + (word >> 1) * 2048 + (word & 1) * 8) =
-            make_uint2(f16x2(x[w][F::place(0, 0)] * up, x[w][F::place(0, 1)] * up),
-                       f16x2(x[w][F::place(1, 0)] * up, x[w][F::place(1, 1)] * up));
+      for (int w = 0; w < W; ++w) {
+        x[w][0] = __uint_as_float(v[k][w].x << 16);
+        x[w][1] = __uint_as_float(v[k][w].x & 0xffff0000u);
+        x[w][2] = __uint_as_float(v[k][w].y << 16);
+        x[w][3] = __uint_as_float(v[k][w].y & 0xffff0000u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[w][e]));
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const int e = big > 0.0f ? max(-100, min(100, 13 - ilogbf(big))) : 0;
+      const float up = pow2i(e);
+      unsigned char* dst = smem + L::Q + (r >> 7) * L::Q_BYTES + (r & 127) * 16;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int word = lane + 32 * w;
+        if (word < D / 4)
+          *reinterpret_cast<uint2*>(dst + (word >> 1) * 2048 + (word & 1) * 8) =
+              make_uint2(f16x2(x[w][F::place(0, 0)] * up, x[w][F::place(0, 1)] * up),
+                         f16x2(x[w][F::place(1, 0)] * up, x[w][F::place(1, 1)] * up));
+      }
+      if (lane == 0) crow[r] = a.attn_scale * kLog2e * pow2i(-e);
     }
-    if (lane == 0) crow[r] = a.attn_scale * kLog2e * pow2i(-e);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   fence_before();
@@ -672,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
     convert_role<F, D, MODE>(a, it, smem, bar, abort, ref, is_v, is_v ? tid - kConvertThreads : tid);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    if (warp == kMmaWarp && it.nt > 0 && lane == 0) mma_role<D, MODE>(it, smem, bar, abort, tbase);
+    if (warp == kMmaWarp && it.nt > 0) mma_role<D, MODE>(it, smem, bar, abort, __shfl_sync(0xffffffffu, tbase, 0));
   }
   __syncwarp();
   fence_before();
@@ -687,8 +701,7 @@ cudaError_t launch_one(const Q8AttendArgs& a, cudaStream_t stream) {
   constexpr int bytes = Layout<D, MODE>::BYTES;
   const cudaError_t e = ensure_smem_limit(tc_kernel<F, D, MODE>, bytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = (int64_t)a.c.B * a.c.Hkv * a.plan.tiles * a.plan.n_chunks;
-  tc_kernel<F, D, MODE><<<(unsigned)grid, kThreads, bytes, stream>>>(a);
+  tc_kernel<F, D, MODE><<<(unsigned)a.plan.items(), kThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
