@@ -14,9 +14,9 @@
 // In each the products of one S run while the softmax of the other does.
 //
 // Warps.  0..3 and 4..7: softmax, a thread per row, so row statistics need no
-// exchange (d = 256: 0..3 only).  8..15 (K, V): conversion of codes to f16 operands in
+// exchange (d = 256: 0..3 only).  8..13 (K, V): conversion of codes to f16 operands in
 // shared memory, loaded from global memory one tile ahead into registers.
-// 16: issues the products.
+// 14: issues the products.
 //
 // Numbers.  Codes and the queries (bf16, scaled by a power of two per row) are
 // exact in f16, so scores carry fp32's rounding alone.  A weight is
@@ -47,15 +47,17 @@ namespace {
 using namespace q8;
 using namespace tc;
 
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;  // (4 for K and 4 for V)
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 3;  // (3 for K and 3 for V)
 constexpr int kMmaWarp = kSoftmaxWarps + 2 * kConvertWarps;
-constexpr int kWarps = 20, kThreads = 32 * kWarps;  // five warpgroups
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kConvertThreads = 32 * kConvertWarps;
-// registers of a thread by role: 2 x 136 + 2 x 72 + 64 = 5 x 96, what the block is launched with
-constexpr int kSoftmaxRegs = 136, kConvertRegs = 72, kMmaRegs = 64;
+// Registers of a thread: 2 x 144 + 2 x 112 = 4 x 128, what the four warpgroups are launched
+// with.  A softmax thread holds 64 scores; what does not fit is spilled to local memory, and
+// L1, which the operands leave next to nothing, misses on half of that.
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 // kCubic of every 8 pairs of exponentials take the cubic on the FMA pipe: 16 a clock and SM
 // would bound the tile (2 x 128 x 128 of them in the 2048 clocks of its products)
-constexpr int kCubic = 1;
+constexpr int kCubic = 2;
 // as in q8_split.cu the reference is held 2^kShift below the maximum it was taken from, and
 // moves when weights reach 2^15
 constexpr float kShift = 7.0f, kTopSum = 32768.0f;
@@ -72,8 +74,8 @@ struct Layout {
   static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = T * D * 2;
   static constexpr int Q = 0, K = Q + QT * Q_BYTES, V = K + 2 * KV_BYTES;
   static constexpr int CROW = V + 2 * KV_BYTES;             // float [QT * 128]
-  static constexpr int SCALES = CROW + 4 * QT * 128;        // float2 [kScaleSlots][T / 16]
-  static constexpr int BAR = SCALES + 8 * kScaleSlots * (T / 16);
+  static constexpr int SCALES = CROW + 4 * QT * 128;        // float4 [kScaleSlots][T / 16]
+  static constexpr int BAR = SCALES + 16 * kScaleSlots * (T / 16);
   static constexpr int MISC = BAR + 8 * 32;                 // tmem base, abort, ref, warp maxima
   static constexpr int BYTES = MISC + 16 + 4 * kWarps;
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -129,16 +131,14 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
 template <int D>
 __device__ __forceinline__ void rescale(uint32_t col, float alpha) {
 #pragma unroll 1
-  for (int c = 0; c < D / 16; ++c) {
-    uint32_t o[16];
-    tld_x16(col + 16 * c, o);
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t o[8];
+    tld_x8(col + 8 * c, o);
     wait_ld();
-    asm volatile("" : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]),
-                 "+r"(o[7]), "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]), "+r"(o[12]), "+r"(o[13]),
-                 "+r"(o[14]), "+r"(o[15]));
+    asm volatile("" : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7]));
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-    tst_x16(col + 16 * c, o);
+    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    tst_x8_quiet(col + 8 * c, o);
   }
 }
 
@@ -163,15 +163,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // One thread's 16-byte pieces of a tile of codes: piece i is bytes 16 c .. of token t with
 // p = thread + kConvertThreads i, t = (p & 7) + 8 ((p >> 3) / C), c = (p >> 3) % C, C = D / 16
-// (8 neighbouring tokens in 8 lanes: their stores fill the banks).
+// (8 neighbouring tokens in 8 lanes: their stores fill the banks).  From one piece to the
+// P-th next, c is the same and t moves by kTokens.
+__host__ __device__ constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 template <int D>
 struct Pieces {
-  static constexpr int T = tile_tokens(D), C = D / 16, N = T * C / kConvertThreads;
-  static constexpr bool kEven = (kConvertThreads / 8) % C == 0;  // all pieces have the same c
+  static constexpr int T = tile_tokens(D), C = D / 16, N = (T * C + kConvertThreads - 1) / kConvertThreads;
+  static constexpr int P = C / gcd(kConvertThreads / 8, C), kTokens = kConvertThreads * P / C;
+  static constexpr bool kRest = T * C % kConvertThreads != 0;  // whole warps have no last piece
   uint4 w[N];
   static __device__ __forceinline__ int token(int p) { return (p & 7) + 8 * ((p >> 3) / C); }
   static __device__ __forceinline__ int c16(int p) { return (p >> 3) % C; }
   static __device__ __forceinline__ int piece(int tid, int i) { return tid + kConvertThreads * i; }
+  static __device__ __forceinline__ bool has(int tid, int i) { return !kRest || i + 1 < N || piece(tid, i) < T * C; }
   __device__ __forceinline__ void load_one(int i, const uint8_t* at) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
@@ -180,32 +184,36 @@ struct Pieces {
   // rows of the tile behind the first `rows` repeat the last one: what is multiplied is
   // always cache content
   __device__ __forceinline__ void load(const uint8_t* tile, int rows, int tid) {
-    if (kEven && rows >= T) {
-      const uint8_t* at = tile + token(tid) * D + 16 * c16(tid);
+    if (rows >= T) {
+      const uint8_t* at[P];
 #pragma unroll
-      for (int i = 0; i < N; ++i) load_one(i, at + i * (kConvertThreads / C) * D);
+      for (int i = 0; i < P; ++i) at[i] = tile + token(piece(tid, i)) * D + 16 * c16(piece(tid, i));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (has(tid, i)) load_one(i, at[i % P] + i / P * kTokens * D);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int p = piece(tid, i);
-        load_one(i, tile + min(token(p), rows - 1) * D + 16 * c16(p));
+        if (has(tid, i)) load_one(i, tile + min(token(p), rows - 1) * D + 16 * c16(p));
       }
     }
   }
   template <typename F>
   __device__ __forceinline__ void store(unsigned char* dst, int tid) const {
+    unsigned char* at[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) at[i] = dst + (2 * c16(piece(tid, i)) * T + token(piece(tid, i))) * 16;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int p = piece(tid, i);
-      unsigned char* at = kEven ? dst + (2 * c16(tid) * T + token(tid)) * 16 + i * (kConvertThreads / C) * 16
-                                : dst + (2 * c16(p) * T + token(p)) * 16;
+      if (!has(tid, i)) continue;
       uint4 lo, hi;
       F::cvt_word(w[i].x, lo.x, lo.y);
       F::cvt_word(w[i].y, lo.z, lo.w);
       F::cvt_word(w[i].z, hi.x, hi.y);
       F::cvt_word(w[i].w, hi.z, hi.w);
-      *reinterpret_cast<uint4*>(at) = lo;
-      *reinterpret_cast<uint4*>(at + T * 16) = hi;
+      *reinterpret_cast<uint4*>(at[i % P] + i / P * kTokens * 16) = lo;
+      *reinterpret_cast<uint4*>(at[i % P] + i / P * kTokens * 16 + T * 16) = hi;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -246,12 +254,13 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
     const int s = j & 1;
     if (j >= 2) warp_wait(empty + s, ((j >> 1) - 1) & 1, abort);
     if (first_k) {
-      // {s_k, log2(s_v / ref)}.  Slot j - 4 has been read: the scores of tile j - 2 came
+      // {s_k, log2(s_v / ref), ref / s_v}.  Slot j - 4 has been read: the scores of tile j - 2 came
       // after the weights of tile j - 4.
       const int slot = j & (kScaleSlots - 1);
       if (scales) {
         const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
-        reinterpret_cast<float2*>(smem + L::SCALES)[slot * (L::T / 16) + tid] = make_float2(sk, log2f(ratio));
+        reinterpret_cast<float4*>(smem + L::SCALES)[slot * (L::T / 16) + tid] =
+            make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + kScFull + slot);
@@ -288,21 +297,18 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
     }
     commit(kSFull + b);
   };
-  // O[u] += P[b] V of token tile j; the weights come in two halves, phase by phase
-  auto values = [&](int j, int u, int b, uint32_t phase, bool first) {
+  // O[u] += P[b] V of half h of token tile j, once its weights are there
+  auto values = [&](int j, int h, int u, int b, uint32_t phase, bool first) {
     const uint32_t v = at + ((L::V + (j & 1) * L::KV_BYTES) >> 4);
     constexpr int H = L::T / 32;  // products of 16 tokens in a half
+    warp_wait(bar + kPFull + 2 * b + h, phase, abort);
+    fence_after();
+    if (leader && !*abort) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      warp_wait(bar + kPFull + 2 * b + h, phase, abort);
-      fence_after();
-      if (leader && !*abort) {
-#pragma unroll
-        for (int c = h * H; c < (h + 1) * H; ++c)
-          mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * c, v0 | (v + c * 16), idO, c > 0 || !first);
-      }
-      commit(kPVDone + 2 * u + h);
+      for (int c = 0; c < H; ++c)
+        mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * (h * H + c), v0 | (v + (h * H + c) * 16), idO, c > 0 || !first);
     }
+    commit(kPVDone + 2 * u + h);
   };
   auto wait_k = [&](int j) {
     warp_wait(bar + kKFull + (j & 1), (j >> 1) & 1, abort);
@@ -322,7 +328,8 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
       wait_v(j);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        values(j, u, u, j & 1, j == 0);
+        values(j, 0, u, u, j & 1, j == 0);
+        values(j, 1, u, u, j & 1, false);
         if (j + 1 < it.nt) {
           if (u == 0) wait_k(j + 1);
           scores(j + 1, u, u);
@@ -339,9 +346,10 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
     }
 #pragma unroll 1
     for (int j = 0; j < it.nt; ++j) {
-      const int b = j & 1;
+      const int b = j & 1, u = MODE == kQ8TwoStreams ? b : 0;
       wait_v(j);
-      values(j, MODE == kQ8TwoStreams ? b : 0, b, (j >> 1) & 1, MODE == kQ8TwoStreams ? j < 2 : j == 0);
+      values(j, 0, u, b, (j >> 1) & 1, MODE == kQ8TwoStreams ? j < 2 : j == 0);
+      values(j, 1, u, b, (j >> 1) & 1, false);
       commit(kVEmpty + b);
       if (j + 2 < it.nt) {
         wait_k(j + 2);
@@ -372,12 +380,13 @@ __device__ __forceinline__ float2 ex2_cubic(float2 x) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// A half tile of H tokens of one row, in registers, and its factors for the scores of
-// each 16 tokens: {s_k crow, log2(s_v / ref)}.
+// A half tile of H tokens of one row: its scores in registers, and for each 16 tokens
+// {s_k, log2(s_v / ref), ref / s_v} in shared memory.  What else a thread keeps is little
+// enough for 128 registers: anything spilled here costs an L2 access per tile, since the
+// operands leave L1 next to nothing.
 template <int H>
 struct Half {
   uint32_t s[H / 32][32];
-  float f[H / 16], lv[H / 16];
 
   __device__ __forceinline__ void load(uint32_t col) {
 #pragma unroll
@@ -387,72 +396,77 @@ struct Half {
     for (int c = 0; c < H / 32; ++c) tie32(s[c]);
   }
   __device__ __forceinline__ float at(int i) const { return __uint_as_float(s[i / 32][i % 32]); }
+  // A factor of 0 (a block of zeros, whose scores are 0 with any factor) must not let
+  // masked scores through.
+  static __device__ __forceinline__ float factor(float s_k, float crow) { return fmaxf(s_k * crow, 1e-30f); }
 
-  // The row sees only the first `left` tokens.  A factor of 0 (a block of zeros, whose
-  // scores are 0 with any factor) must not let the others through.
+  // the row sees only the first `left` tokens
   __device__ __forceinline__ void mask(int left) {
 #pragma unroll
     for (int i = 0; i < H; ++i)
       if (i >= left) s[i / 32][i % 32] = __float_as_uint(kMasked);
-#pragma unroll
-    for (int g = 0; g < H / 16; ++g) f[g] = fmaxf(f[g], 1e-30f);
   }
 
   // the largest score in log2 units
-  __device__ __forceinline__ float max() const {
+  __device__ __forceinline__ float max(const float4* sc, float crow) const {
     float mx = -INFINITY;
 #pragma unroll
     for (int g = 0; g < H / 16; ++g) {
       float top = at(16 * g);
 #pragma unroll
       for (int i = 16 * g + 1; i < 16 * g + 16; ++i) top = fmaxf(top, at(i));
-      mx = fmaxf(mx, top * f[g]);
+      mx = fmaxf(mx, top * factor(sc[g].x, crow));
     }
     return mx;
   }
 
-  // The weights 2^(x + lv - m), into tensor memory over scores already read.  Returns their
-  // sum without the factors 2^lv; top is the largest sum of 16 with them.
-  __device__ __forceinline__ float weights(uint32_t col, float m, float& top) const {
+  // The weights 2^(x + log2(s_v / ref) - m), into tensor memory over scores already read.
+  // Returns the sum of 2^(x - m); top is the largest sum of 16 weights.
+  __device__ __forceinline__ float weights(uint32_t col, const float4* sc, float crow, float m, float& top) const {
     float l = 0.0f;
     top = 0.0f;
+    float4 k = sc[0];
 #pragma unroll
-    for (int c = 0; c < H / 32; ++c) {
-      uint32_t w[16];
+    for (int g = 0; g < H / 16; ++g) {
+      const float4 now = k;
+      if (g + 1 < H / 16) k = sc[g + 1];
+      const float f = factor(now.x, crow), off = now.y - m;
+      float2 x[8];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int g = 2 * c + e;
-        const float2 f2 = make_float2(f[g], f[g]), off = make_float2(lv[g] - m, lv[g] - m);
-        float2 x[8];
+      for (int i = 0; i < 8; ++i)
+        x[i] = fma2(make_float2(at(16 * g + 2 * i), at(16 * g + 2 * i + 1)), make_float2(f, f), make_float2(off, off));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fma2(make_float2(at(16 * g + 2 * i), at(16 * g + 2 * i + 1)), f2, off);
+      for (int i = 0; i < 8; ++i)
+        x[i] = i * kCubic / 8 != (i + 1) * kCubic / 8 ? ex2_cubic(x[i]) : make_float2(ex2(x[i].x), ex2(x[i].y));
+      uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[i] = i * kCubic / 8 != (i + 1) * kCubic / 8 ? ex2_cubic(x[i]) : make_float2(ex2(x[i].x), ex2(x[i].y));
-        const float2 s2 = add2(add2(add2(x[0], x[1]), add2(x[2], x[3])), add2(add2(x[4], x[5]), add2(x[6], x[7])));
-        const float sum = s2.x + s2.y;
-        top = fmaxf(top, sum);
-        l = fmaf(sum, ex2(-lv[g]), l);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[8 * e + i] = f16x2(x[i].x, x[i].y);
-      }
-      tst_x16(col + 16 * c, w);
+      for (int i = 0; i < 8; ++i) w[i] = f16x2(x[i].x, x[i].y);
+      tst_x8_quiet(col + 8 * g, w);
+      const float2 s2 = add2(add2(add2(x[0], x[1]), add2(x[2], x[3])), add2(add2(x[4], x[5]), add2(x[6], x[7])));
+      const float sum = s2.x + s2.y;
+      top = fmaxf(top, sum);
+      l = fmaf(sum, now.z, l);
     }
     return l;
   }
 };
 
 template <typename F, int D, int MODE>
-__device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& it, const Q8Seq& seq,
+__device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, int stop, int nt, const Q8Seq& seq,
                                              unsigned char* smem, uint64_t* bar, volatile int* abort,
                                              uint32_t tbase, float ref) {
   using L = Layout<D, MODE>;
   constexpr int T = L::T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = warp >> 2, quarter = warp & 3;
   const int local = (MODE == kQ8TwoRows ? 128 * u : 0) + 32 * quarter + lane;
-  const int r = it.row0 + local, i = r / it.G;
-  const bool live = r < it.rows && i < seq.q_len;
-  const int limit = live ? seq.limit(i) : INT_MAX;
+  int limit = INT_MAX;  // (of a row of no query)
+  bool live = false;
+  {
+    const Item it(a, blockIdx.x);
+    const int i = it.token(local);
+    live = it.row0 + local < it.rows && i < seq.q_len;
+    if (live) limit = seq.limit(i);
+  }
   const bool warp_live = __any_sync(0xffffffffu, live);
   const int open = __reduce_min_sync(0xffffffffu, limit);  // tokens below are seen by the whole warp
   const float crow = reinterpret_cast<const float*>(smem + L::CROW)[local];
@@ -462,12 +476,12 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
   constexpr int step = MODE == kQ8TwoStreams ? 2 : 1;
   const int ou = MODE == kQ8OneStream ? 0 : u;
   int n = 0;  // tiles done
-  for (int j = MODE == kQ8TwoStreams ? u : 0; j < it.nt; j += step, ++n) {
+  for (int j = MODE == kQ8TwoStreams ? u : 0; j < nt; j += step, ++n) {
     const int sb = MODE == kQ8TwoRows ? u : (j & 1);
     const int phase = MODE == kQ8TwoRows ? j : (j >> 1);
     const uint32_t s_col = tbase + lanes + L::S(sb);
     warp_wait(bar + kScFull + (j & (kScaleSlots - 1)), (j / kScaleSlots) & 1, abort);
-    const float2* sc = reinterpret_cast<const float2*>(smem + L::SCALES) + (j & (kScaleSlots - 1)) * (T / 16);
+    const float4* sc = reinterpret_cast<const float4*>(smem + L::SCALES) + (j & (kScaleSlots - 1)) * (T / 16);
     warp_wait(bar + kSFull + sb, phase & 1, abort);
     fence_after();
     // Each half is a step of the online softmax of its own: its product starts while the
@@ -480,21 +494,16 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
       if (warp_live) {
         constexpr int H = T / 2;
         Half<H> x;
-#pragma unroll
-        for (int g = 0; g < H / 16; ++g) {
-          const float2 k = sc[h * (H / 16) + g];
-          x.f[g] = k.x * crow;
-          x.lv[g] = k.y;
-        }
-        const int tok0 = it.begin + j * T + h * H;
-        const int left = min(limit, it.stop) - tok0;  // tokens of this half that the row sees
+        const float4* sch = sc + h * (H / 16);
+        const int tok0 = begin + j * T + h * H;
+        const int left = min(limit, stop) - tok0;  // tokens of this half that the row sees
         x.load(s_col + h * H);
-        if (tok0 + H > min(open, it.stop)) x.mask(left);
+        if (tok0 + H > min(open, stop)) x.mask(left);
         const uint32_t p_col = s_col + h * (H / 2);
-        float top, sum = x.weights(p_col, m == -INFINITY ? 0.0f : m, top);
+        float top, sum = x.weights(p_col, sch, crow, m == -INFINITY ? 0.0f : m, top);
         const bool move = top > kTopSum || m == -INFINITY;
         if (__any_sync(0xffffffffu, move)) {
-          const float mn = move && left > 0 ? fmaxf(m, x.max() - kShift) : m;  // m is held 2^kShift low
+          const float mn = move && left > 0 ? fmaxf(m, x.max(sch, crow) - kShift) : m;  // m is held 2^kShift low
           const float alpha = mn == m ? 1.0f : exp2f(m - mn);
           m = mn;
           l *= alpha;
@@ -505,7 +514,7 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
             rescale<D>(tbase + lanes + L::O(ou), alpha);
           }
           wait_st();
-          sum = x.weights(p_col, m == -INFINITY ? 0.0f : m, top);
+          sum = x.weights(p_col, sch, crow, m == -INFINITY ? 0.0f : m, top);
         }
         l += sum;
         wait_st();
@@ -515,11 +524,15 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, const Item& 
       if (lane == 0) mbar_arrive(bar + kPFull + 2 * sb + h);
     }
   }
-  if (it.nt > 0) warp_wait(bar + kDone, 0, abort);
+  if (nt > 0) warp_wait(bar + kDone, 0, abort);
   fence_after();
   if (!warp_live) return;
   const bool none = n == 0 || (m == -INFINITY && l < 1e-20f);  // (masked weights of the cubic are 2^-126)
   if (none) l = 0.0f;
+  // where the row goes, worked out anew rather than kept in registers through the loop
+  int id;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(id));
+  const Item it(a, id);
   const int64_t orow = it.out_row(a, local);
   const bool split = it.split;
   if (*abort) l = __int_as_float(0x7fc00000);
@@ -675,17 +688,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, warp_max[w]);
 
-  if (warp < kSoftmaxWarps) {
+  if (warp >= kSoftmaxWarps)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  else
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  if (warp < kSoftmaxWarps) {
     if (MODE != kQ8OneStream || warp < 4)
-      softmax_role<F, D, MODE>(a, it, seq, smem, bar, abort, tbase, ref);
+      softmax_role<F, D, MODE>(a, it.begin, it.stop, it.nt, seq, smem, bar, abort, tbase, ref);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
     const int tid = threadIdx.x - 32 * kSoftmaxWarps;
     const bool is_v = tid >= kConvertThreads;
     convert_role<F, D, MODE>(a, it, smem, bar, abort, ref, is_v, is_v ? tid - kConvertThreads : tid);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (warp == kMmaWarp && it.nt > 0) mma_role<D, MODE>(it, smem, bar, abort, __shfl_sync(0xffffffffu, tbase, 0));
   }
   __syncwarp();
