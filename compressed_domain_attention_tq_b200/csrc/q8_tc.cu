@@ -184,26 +184,24 @@ struct Pieces {
   // rows of the tile behind the first `rows` repeat the last one: what is multiplied is
   // always cache content
   __device__ __forceinline__ void load(const uint8_t* tile, int rows, int tid) {
-    if (rows >= T) {
-      const uint8_t* at[P];
 #pragma unroll
-      for (int i = 0; i < P; ++i) at[i] = tile + token(piece(tid, i)) * D + 16 * c16(piece(tid, i));
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (has(tid, i)) load_one(i, at[i % P] + i / P * kTokens * D);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int p = piece(tid, i);
-        if (has(tid, i)) load_one(i, tile + min(token(p), rows - 1) * D + 16 * c16(p));
-      }
+    for (int i = 0; i < N; ++i) {
+      const int p = piece(tid, i);
+      if (has(tid, i)) load_one(i, tile + min(token(p), rows - 1) * D + 16 * c16(p));
     }
   }
-  template <typename F>
-  __device__ __forceinline__ void store(unsigned char* dst, int tid) const {
+  // Stores the operand.  Where the next tile is whole each register is loaded again as soon
+  // as its piece is stored, so that a load has the time of a whole tile to arrive.
+  template <typename F, bool NEXT>
+  __device__ __forceinline__ void store(unsigned char* dst, const uint8_t* next, int tid) {
     unsigned char* at[P];
+    const uint8_t* from[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) at[i] = dst + (2 * c16(piece(tid, i)) * T + token(piece(tid, i))) * 16;
+    for (int i = 0; i < P; ++i) {
+      const int p = piece(tid, i);
+      at[i] = dst + (2 * c16(p) * T + token(p)) * 16;
+      from[i] = next + token(p) * D + 16 * c16(p);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!has(tid, i)) continue;
@@ -214,6 +212,7 @@ struct Pieces {
       F::cvt_word(w[i].w, hi.z, hi.w);
       *reinterpret_cast<uint4*>(at[i % P] + i / P * kTokens * 16) = lo;
       *reinterpret_cast<uint4*>(at[i % P] + i / P * kTokens * 16 + T * 16) = hi;
+      if constexpr (NEXT) load_one(i, from[i % P] + i / P * kTokens * D);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -237,18 +236,14 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
   unsigned char* operand = smem + (is_v ? L::V : L::K);
   Pieces<D> x;
   float sk = 0.0f, sv = 0.0f;
-  auto load = [&](int j) {
-    if (j >= it.nt) return;
-    const int tok0 = it.begin + j * L::T;
-    if (scales) {
-      const int blk = min(tok0 + 16 * tid, it.stop - 1) >> shift;
-      sk = __ldg(ksc + blk);
-      sv = __ldg(vsc + blk);
-    }
-    x.load(tile, it.stop - tok0, tid);
-    tile += L::T * D;
+  auto load_scales = [&](int j) {
+    if (!scales || j >= it.nt) return;
+    const int blk = min(it.begin + j * L::T + 16 * tid, it.stop - 1) >> shift;
+    sk = __ldg(ksc + blk);
+    sv = __ldg(vsc + blk);
   };
-  load(0);
+  load_scales(0);
+  if (it.nt > 0) x.load(tile, it.stop - it.begin, tid);
 #pragma unroll 1
   for (int j = 0; j < it.nt; ++j) {
     const int s = j & 1;
@@ -264,10 +259,16 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + kScFull + slot);
+      load_scales(j + 1);
     }
-    x.template store<F>(operand + s * L::KV_BYTES, tid);
+    tile += L::T * D;
+    const int rows = it.stop - it.begin - (j + 1) * L::T;  // of the next tile
+    if (rows >= L::T)
+      x.template store<F, true>(operand + s * L::KV_BYTES, tile, tid);
+    else
+      x.template store<F, false>(operand + s * L::KV_BYTES, tile, tid);
     if (lane == 0 && !(a.test_starve && !is_v && j == 0)) mbar_arrive(full + s);
-    load(j + 1);
+    if (rows > 0 && rows < L::T) x.load(tile, rows, tid);
   }
 }
 
