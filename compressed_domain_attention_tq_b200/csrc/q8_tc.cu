@@ -16,7 +16,7 @@
 // Warps.  0..3 and 4..7: softmax, a thread per row, so row statistics need no
 // exchange (d = 256: 0..3 only).  8..13 (K, V): conversion of codes to f16 operands in
 // shared memory, loaded from global memory one tile ahead into registers.
-// 14: issues the products.
+// 14: issues the products; 15: the blocks' scales.
 //
 // Numbers.  Codes and the queries (bf16, scaled by a power of two per row) are
 // exact in f16, so scores carry fp32's rounding alone.  A weight is
@@ -48,7 +48,7 @@ using namespace q8;
 using namespace tc;
 
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 3;  // (3 for K and 3 for V)
-constexpr int kMmaWarp = kSoftmaxWarps + 2 * kConvertWarps;
+constexpr int kMmaWarp = kSoftmaxWarps + 2 * kConvertWarps, kScaleWarp = kMmaWarp + 1;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kConvertThreads = 32 * kConvertWarps;
 // Registers of a thread: 2 x 144 + 2 x 112 = 4 x 128, what the four warpgroups are launched
@@ -71,6 +71,9 @@ template <int D, int MODE>
 struct Layout {
   static constexpr int T = tile_tokens(D);
   static constexpr int QT = MODE == kQ8TwoRows ? 2 : 1;
+  // Row r of a tile sits at place r ^ kRowFlip: up to 64 rows then belong to the warps of the
+  // two schedulers that have one converter each, not two (5 drafts at 128K: FLIP_TIMES).
+  static constexpr int kRowFlip = MODE == kQ8TwoRows ? 0 : 64;
   static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = T * D * 2;
   static constexpr int Q = 0, K = Q + QT * Q_BYTES, V = K + 2 * KV_BYTES;
   static constexpr int CROW = V + 2 * KV_BYTES;             // float [QT * 128]
@@ -91,7 +94,7 @@ enum Bar : int {
   kSFull = 8,    // [2] scores in tensor memory (commit)
   kPFull = 10,   // [2][2] the halves of the weights in tensor memory (4 softmax warps)
   kPVDone = 14,  // [2][2] O up to date with that half of a tile (commit)
-  kScFull = 18,  // [kScaleSlots] block scales written (one convert warp)
+  kScFull = 18,  // [kScaleSlots] block scales written (one warp)
   kDone = 22,    // every product complete (commit)
   kBars = 23
 };
@@ -223,44 +226,19 @@ struct Pieces {
 // cache), which keeps two tiles in flight.
 template <typename F, int D, int MODE>
 __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& it, unsigned char* smem,
-                                             uint64_t* bar, volatile int* abort, float ref, bool is_v, int tid) {
+                                             uint64_t* bar, volatile int* abort, bool is_v, int tid) {
   using L = Layout<D, MODE>;
   const int lane = tid & 31;
   const uint8_t* tile = head_codes<D>(is_v ? a.c.v_codes : a.c.k_codes, a, it.bh) + (int64_t)it.begin * D;
-  const float* ksc = a.c.k_scales + (int64_t)it.bh * a.c.n_blocks();
-  const float* vsc = a.c.v_scales + (int64_t)it.bh * a.c.n_blocks();
-  const int shift = 31 - __clz(a.c.block);
-  const bool first_k = !is_v && tid < 32, scales = first_k && tid < L::T / 16;  // 16 tokens a thread
   uint64_t* full = bar + (is_v ? kVFull : kKFull);
   uint64_t* empty = bar + (is_v ? kVEmpty : kKEmpty);
   unsigned char* operand = smem + (is_v ? L::V : L::K);
   Pieces<D> x;
-  float sk = 0.0f, sv = 0.0f;
-  auto load_scales = [&](int j) {
-    if (!scales || j >= it.nt) return;
-    const int blk = min(it.begin + j * L::T + 16 * tid, it.stop - 1) >> shift;
-    sk = __ldg(ksc + blk);
-    sv = __ldg(vsc + blk);
-  };
-  load_scales(0);
   if (it.nt > 0) x.load(tile, it.stop - it.begin, tid);
 #pragma unroll 1
   for (int j = 0; j < it.nt; ++j) {
     const int s = j & 1;
     if (j >= 2) warp_wait(empty + s, ((j >> 1) - 1) & 1, abort);
-    if (first_k) {
-      // {s_k, log2(s_v / ref), ref / s_v}.  Slot j - 4 has been read: the scores of tile j - 2 came
-      // after the weights of tile j - 4.
-      const int slot = j & (kScaleSlots - 1);
-      if (scales) {
-        const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
-        reinterpret_cast<float4*>(smem + L::SCALES)[slot * (L::T / 16) + tid] =
-            make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar + kScFull + slot);
-      load_scales(j + 1);
-    }
     tile += L::T * D;
     const int rows = it.stop - it.begin - (j + 1) * L::T;  // of the next tile
     if (rows >= L::T)
@@ -269,6 +247,38 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
       x.template store<F, false>(operand + s * L::KV_BYTES, tile, tid);
     if (lane == 0 && !(a.test_starve && !is_v && j == 0)) mbar_arrive(full + s);
     if (rows > 0 && rows < L::T) x.load(tile, rows, tid);
+  }
+}
+
+// For each 16 tokens of a tile {s_k, log2(s_v / ref), ref / s_v}: a warp of its own, since
+// the logarithm and the divisions held a converter up for a third of its time.
+template <int D, int MODE>
+__device__ __forceinline__ void scale_role(const Q8AttendArgs& a, const Item& it, unsigned char* smem,
+                                           uint64_t* bar, volatile int* abort, float ref, int lane) {
+  using L = Layout<D, MODE>;
+  const float* ksc = a.c.k_scales + (int64_t)it.bh * a.c.n_blocks();
+  const float* vsc = a.c.v_scales + (int64_t)it.bh * a.c.n_blocks();
+  const int shift = 31 - __clz(a.c.block);
+  float sk = 0.0f, sv = 0.0f;
+  auto load = [&](int j) {
+    if (lane >= L::T / 16 || j >= it.nt) return;
+    const int blk = min(it.begin + j * L::T + 16 * lane, it.stop - 1) >> shift;
+    sk = __ldg(ksc + blk);
+    sv = __ldg(vsc + blk);
+  };
+  load(0);
+#pragma unroll 1
+  for (int j = 0; j < it.nt; ++j) {
+    const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
+    const float4 k = make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
+    load(j + 1);
+    // slot j - 4 has been read once the scores of tile j - 2 are done: they came after the
+    // weights of tile j - 4
+    const int slot = j & (kScaleSlots - 1);
+    if (j >= 2) warp_wait(bar + kKEmpty + (j & 1), ((j >> 1) - 1) & 1, abort);
+    if (lane < L::T / 16) reinterpret_cast<float4*>(smem + L::SCALES)[slot * (L::T / 16) + lane] = k;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + kScFull + slot);
   }
 }
 
@@ -459,7 +469,7 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
   using L = Layout<D, MODE>;
   constexpr int T = L::T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = warp >> 2, quarter = warp & 3;
-  const int local = (MODE == kQ8TwoRows ? 128 * u : 0) + 32 * quarter + lane;
+  const int local = ((MODE == kQ8TwoRows ? 128 * u : 0) + 32 * quarter + lane) ^ L::kRowFlip;
   int limit = INT_MAX;  // (of a row of no query)
   bool live = false;
   {
@@ -668,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
       for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
       const int e = big > 0.0f ? max(-100, min(100, 13 - ilogbf(big))) : 0;
       const float up = pow2i(e);
-      unsigned char* dst = smem + L::Q + (r >> 7) * L::Q_BYTES + (r & 127) * 16;
+      unsigned char* dst = smem + L::Q + (r >> 7) * L::Q_BYTES + ((r ^ L::kRowFlip) & 127) * 16;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int word = lane + 32 * w;
@@ -699,9 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   } else if (warp < kMmaWarp) {
     const int tid = threadIdx.x - 32 * kSoftmaxWarps;
     const bool is_v = tid >= kConvertThreads;
-    convert_role<F, D, MODE>(a, it, smem, bar, abort, ref, is_v, is_v ? tid - kConvertThreads : tid);
+    convert_role<F, D, MODE>(a, it, smem, bar, abort, is_v, is_v ? tid - kConvertThreads : tid);
+  } else if (warp == kScaleWarp) {
+    scale_role<D, MODE>(a, it, smem, bar, abort, ref, lane);
   } else {
-    if (warp == kMmaWarp && it.nt > 0) mma_role<D, MODE>(it, smem, bar, abort, __shfl_sync(0xffffffffu, tbase, 0));
+    if (it.nt > 0) mma_role<D, MODE>(it, smem, bar, abort, __shfl_sync(0xffffffffu, tbase, 0));
   }
   __syncwarp();
   fence_before();
