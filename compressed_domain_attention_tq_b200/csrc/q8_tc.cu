@@ -27,10 +27,9 @@
 // a block whose scale is that far below ref then counts with at most
 // 2^-40 max|v|, far below the output's rounding.  Row sums and O are fp32.
 //
-// Operand layout in shared memory, without swizzle: [d / 8][rows][16 bytes], an
-// 8 x 16-byte core matrix contiguous.  For K that is K-major (rows = tokens), and
-// the same bytes are MN-major for V, so one converter serves both, and its
-// 16-byte stores of 8 neighbouring tokens fill all banks.  int8 codes leave the
+// Operand layout in shared memory, without swizzle: [d / 8][rows][16 bytes] (and a pad
+// after each column of rows), an 8 x 16-byte core matrix contiguous.  For K that is K-major (rows = tokens), and
+// the same bytes are MN-major for V, so one converter serves both.  int8 codes leave the
 // converter in the order 0 2 1 3 of each word: Q is stored in that order, and
 // O's columns are put back when they are written.
 //
@@ -62,10 +61,11 @@ constexpr int kCubic = 2;
 // moves when weights reach 2^15
 constexpr float kShift = 7.0f, kTopSum = 32768.0f;
 constexpr float kMasked = -3e38f, kMinRatio = 0x1p-40f;
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 4, kPrefetch = 2;
 
-// tokens of a tile, row tiles in shared memory
+// tokens of a tile; what a column of its operands (8 dims of all tokens) is longer than them
 __host__ __device__ constexpr int tile_tokens(int d) { return d <= 128 ? 128 : 64; }
+__host__ __device__ constexpr int column_pad(int d) { return d == 96 ? 32 : 16; }
 
 template <int D, int MODE>
 struct Layout {
@@ -74,7 +74,7 @@ struct Layout {
   // Row r of a tile sits at place r ^ kRowFlip: up to 64 rows then belong to the warps of the
   // two schedulers that have one converter each, not two (5 drafts at 128K: FLIP_TIMES).
   static constexpr int kRowFlip = MODE == kQ8TwoRows ? 0 : 64;
-  static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = T * D * 2;
+  static constexpr int Q_BYTES = 128 * D * 2, COLUMN = T * 16 + column_pad(D), KV_BYTES = D / 8 * COLUMN;
   static constexpr int Q = 0, K = Q + QT * Q_BYTES, V = K + 2 * KV_BYTES;
   static constexpr int CROW = V + 2 * KV_BYTES;             // float [QT * 128]
   static constexpr int SCALES = CROW + 4 * QT * 128;        // float4 [kScaleSlots][T / 16]
@@ -164,19 +164,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // ------------------------------------------------------------------ conversion
 
-// One thread's 16-byte pieces of a tile of codes: piece i is bytes 16 c .. of token t with
-// p = thread + kConvertThreads i, t = (p & 7) + 8 ((p >> 3) / C), c = (p >> 3) % C, C = D / 16
-// (8 neighbouring tokens in 8 lanes: their stores fill the banks).  From one piece to the
-// P-th next, c is the same and t moves by kTokens.
-__host__ __device__ constexpr int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+// One thread's 16-byte pieces of a tile of codes, p = thread + kConvertThreads i.  Eight
+// neighbouring lanes take kC pieces of each of kT tokens: a load touches few lines (with
+// eight tokens a load it took 28 clocks of the SM, not 8), and with the columns of the
+// operand kPad bytes further apart their stores fill all banks.
 template <int D>
 struct Pieces {
   static constexpr int T = tile_tokens(D), C = D / 16, N = (T * C + kConvertThreads - 1) / kConvertThreads;
-  static constexpr int P = C / gcd(kConvertThreads / 8, C), kTokens = kConvertThreads * P / C;
+  static constexpr int kC = D == 96 ? 2 : 4, kT = 8 / kC, kPad = column_pad(D);
+  static constexpr int kStep = kConvertThreads / C;  // tokens from one piece of a thread to the next
+  static_assert(kConvertThreads % (8 * C / kC) == 0, "a thread's pieces are the same bytes of their tokens");
   static constexpr bool kRest = T * C % kConvertThreads != 0;  // whole warps have no last piece
   uint4 w[N];
-  static __device__ __forceinline__ int token(int p) { return (p & 7) + 8 * ((p >> 3) / C); }
-  static __device__ __forceinline__ int c16(int p) { return (p >> 3) % C; }
+  static __device__ __forceinline__ int token(int p) { return p / kC % kT + kT * ((p >> 3) / (C / kC)); }
+  static __device__ __forceinline__ int c16(int p) { return p % kC + kC * ((p >> 3) % (C / kC)); }
   static __device__ __forceinline__ int piece(int tid, int i) { return tid + kConvertThreads * i; }
   static __device__ __forceinline__ bool has(int tid, int i) { return !kRest || i + 1 < N || piece(tid, i) < T * C; }
   __device__ __forceinline__ void load_one(int i, const uint8_t* at) {
@@ -197,14 +198,9 @@ struct Pieces {
   // as its piece is stored, so that a load has the time of a whole tile to arrive.
   template <typename F, bool NEXT>
   __device__ __forceinline__ void store(unsigned char* dst, const uint8_t* next, int tid) {
-    unsigned char* at[P];
-    const uint8_t* from[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int p = piece(tid, i);
-      at[i] = dst + (2 * c16(p) * T + token(p)) * 16;
-      from[i] = next + token(p) * D + 16 * c16(p);
-    }
+    constexpr int column = T * 16 + kPad;
+    unsigned char* at = dst + 2 * c16(tid) * column + token(tid) * 16;
+    const uint8_t* from = next + token(tid) * D + 16 * c16(tid);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!has(tid, i)) continue;
@@ -213,9 +209,9 @@ struct Pieces {
       F::cvt_word(w[i].y, lo.z, lo.w);
       F::cvt_word(w[i].z, hi.x, hi.y);
       F::cvt_word(w[i].w, hi.z, hi.w);
-      *reinterpret_cast<uint4*>(at[i % P] + i / P * kTokens * 16) = lo;
-      *reinterpret_cast<uint4*>(at[i % P] + i / P * kTokens * 16 + T * 16) = hi;
-      if constexpr (NEXT) load_one(i, from[i % P] + i / P * kTokens * D);
+      *reinterpret_cast<uint4*>(at + i * kStep * 16) = lo;
+      *reinterpret_cast<uint4*>(at + i * kStep * 16 + column) = hi;
+      if constexpr (NEXT) load_one(i, from + i * kStep * D);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -250,6 +246,8 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
   }
 }
 
+// Codes are brought into L2 kPrefetch tiles before the converters load them: their registers
+// hold one tile of K and one of V, 32 KB an SM, which at HBM's latency is 3 TB/s.
 // For each 16 tokens of a tile {s_k, log2(s_v / ref), ref / s_v}: a warp of its own, since
 // the logarithm and the divisions held a converter up for a third of its time.
 template <int D, int MODE>
@@ -266,9 +264,20 @@ __device__ __forceinline__ void scale_role(const Q8AttendArgs& a, const Item& it
     sk = __ldg(ksc + blk);
     sv = __ldg(vsc + blk);
   };
+  // codes of tile j into L2
+  const uint8_t* kc = head_codes<D>(a.c.k_codes, a, it.bh);
+  const uint8_t* vc = head_codes<D>(a.c.v_codes, a, it.bh);
+  auto prefetch = [&](int j) {
+    if (j >= it.nt || lane != 0) return;
+    const int tok0 = it.begin + j * L::T, bytes = min(L::T, it.stop - tok0) * D;
+    prefetch_l2(kc + (int64_t)tok0 * D, bytes);
+    prefetch_l2(vc + (int64_t)tok0 * D, bytes);
+  };
+  for (int j = 1; j < kPrefetch; ++j) prefetch(j);
   load(0);
 #pragma unroll 1
   for (int j = 0; j < it.nt; ++j) {
+    prefetch(j + kPrefetch);
     const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
     const float4 k = make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
     load(j + 1);
@@ -292,7 +301,7 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
   using L = Layout<D, MODE>;
   constexpr uint32_t idS = idesc_f16(128, L::T, 0, 0), idO = idesc_f16(128, D, 0, 1);
   // descriptors: the upper words are constants, the lower ones add (bytes / 16) offsets
-  constexpr uint64_t q0 = smem_desc(0, 128 * 16, 128), k0 = smem_desc(0, L::T * 16, 128), v0 = smem_desc(0, 128, L::T * 16);
+  constexpr uint64_t q0 = smem_desc(0, 128 * 16, 128), k0 = smem_desc(0, L::COLUMN, 128), v0 = smem_desc(0, 128, L::COLUMN);
   const uint32_t at = smem_u32(smem) >> 4;
   const bool leader = elect_one();
   auto commit = [&](int b) {
@@ -304,7 +313,7 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
     if (leader && !*abort) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
-        mma_ss(tbase + L::S(b), q0 | (q + c * 2 * 128), k0 | (k + c * 2 * L::T), idS, c > 0);
+        mma_ss(tbase + L::S(b), q0 | (q + c * 2 * 128), k0 | (k + c * 2 * (L::COLUMN >> 4)), idS, c > 0);
     }
     commit(kSFull + b);
   };
