@@ -56,31 +56,53 @@ __device__ __forceinline__ int v_offset(int w, int g) {
   return w < 2 ? 8 * g + 4 * w : 64 + 4 * g;  // 64, 96
 }
 
-template <int N>
-__device__ __forceinline__ void ld(uint32_t* r, const uint8_t* p) {
-  if constexpr (N == 4)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p));
-  else if constexpr (N == 2)
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
-  else
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+// A warp's ring of steps in shared memory: 16 rows of K, 16 of V, their two scales.
+// 16-byte chunks are placed so that the fragment loads of eight lanes (K: two rows, four
+// chunks; V: four rows, two chunks) meet no bank twice.
+template <int D, int NT = 1>
+struct Ring {
+  // as many steps as leave room for the CTAs that the registers allow (resident())
+  static constexpr int kRows = kStep * D, kBytes = 2 * kRows + 16, kSlots = D == 64 ? 4 : D == 256 && NT == 2 ? 2 : 3;
+  static __device__ __forceinline__ int k_chunk(int row, int ch) { return D >= 128 ? ch ^ ((row & 1) << 2) : ch; }
+  static __device__ __forceinline__ int v_chunk(int row, int ch) {
+    return D >= 128 ? ch ^ (row & 6) : D == 64 ? ch ^ (row & 2) : ch;
+  }
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void ld(uint32_t* r, const unsigned char* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x, r[1] = v.y;
+  } else {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// K words of token row g (or g + 8) of lane t; V words of token row 2t (+ 1, 8, 9) of lane g
 template <int D>
-__device__ __forceinline__ void load_k(uint32_t (&r)[D / 16], const uint8_t* row, int t) {
+__device__ __forceinline__ void load_k(uint32_t (&r)[D / 16], const unsigned char* row, int g, int t) {
 #pragma unroll
-  for (int w = 0; w + 4 <= D / 16; w += 4) ld<4>(r + w, row + k_offset<D>(w, t));
+  for (int w = 0; w + 4 <= D / 16; w += 4) ld<4>(r + w, row + 16 * Ring<D>::k_chunk(g, 4 * (w >> 2) + t));
   if constexpr (D % 64) ld<2>(r + D / 64 * 4, row + k_offset<D>(D / 64 * 4, t));
 }
 template <int D>
-__device__ __forceinline__ void load_v(uint32_t (&r)[D / 32], const uint8_t* row, int g) {
+__device__ __forceinline__ void load_v(uint32_t (&r)[D / 32], const unsigned char* row, int g, int t) {
   if constexpr (D >= 128) {
 #pragma unroll
-    for (int w = 0; w < D / 32; w += 4) ld<4>(r + w, row + v_offset<D>(w, g));
+    for (int w = 0; w < D / 32; w += 4) ld<4>(r + w, row + 16 * Ring<D>::v_chunk(2 * t, 8 * (w >> 2) + g));
   } else {
-    ld<2>(r, row + v_offset<D>(0, g));
+    ld<2>(r, row + 16 * Ring<D>::v_chunk(2 * t, g >> 1) + 8 * (g & 1));
     if constexpr (D == 96) ld<1>(r + 2, row + v_offset<D>(2, g));
   }
 }
@@ -106,12 +128,16 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = tc::f16x2(x - h.x, y - h.y);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool LO>
 struct Smem {
-  uint4 q[NT][D / 16][32];          // query fragments: hi pair 0, hi pair 1, lo pair 0, lo pair 1
+  // query fragments: hi pair 0, hi pair 1, and lo pair 0, lo pair 1 where queries have a lo part
+  uint2 q[NT][D / 16][LO ? 2 : 1][32];
   float crow[8 * NT];               // scale of a row's sums: attn_scale log2(e) 2^-e
   float m[kWarps][8 * NT], l[kWarps][8 * NT], ref[kWarps];
-  float acc[kWarps][8][D + 4];      // a row tile's sums of each warp (rows padded against bank conflicts)
+  union {
+    alignas(16) unsigned char ring[kWarps][Ring<D, NT>::kSlots][Ring<D, NT>::kBytes];
+    float acc[kWarps][8][D + 4];    // a row tile's sums of each warp (rows padded against bank conflicts)
+  };
 };
 
 // One query element in fp32.
@@ -125,11 +151,12 @@ __device__ __forceinline__ float q_elem(const Q8AttendArgs& a, int64_t row, int 
 // step's codes and the queries' row state: 64 d NT / 32 + d / 4 + ...).
 constexpr int resident(int d, int nt) { return d == 256 ? 2 : d == 128 ? 5 - nt : nt == 1 ? 5 : 4; }
 
-template <typename F, int D, int NT>
+template <typename F, int D, int NT, bool LO>
 __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8AttendArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
-  Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(raw);
+  Smem<D, NT, LO>& sm = *reinterpret_cast<Smem<D, NT, LO>*>(raw);
   constexpr int KW = D / 16, VW = D / 32, MT = D / 16;
+  using R = Ring<D, NT>;
   const Q8Cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const Q8Item it(a, blockIdx.x);
@@ -146,6 +173,33 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   const int begin = it.chunk_id * a.plan.chunk;
   const int stop = it.split ? min(stop_all, begin + a.plan.chunk) : stop_all;
   if (begin >= stop && it.split) return;
+
+  const uint8_t* kc = c.k_codes + (int64_t)bh * c.capacity * D;
+  const uint8_t* vc = c.v_codes + (int64_t)bh * c.capacity * D;
+  const float* ksc = c.k_scales + (int64_t)bh * c.n_blocks();
+  const float* vsc = c.v_scales + (int64_t)bh * c.n_blocks();
+  const int shift = 31 - __clz(c.block);
+
+  // step `tok` into slot `slot` (rows behind the last one repeat it, so what a lane multiplies
+  // is always cache content); an empty group where there is none
+  const uint32_t ring = tc::smem_u32(sm.ring[warp]);
+  auto fetch = [&](int tok, int slot) {
+    if (tok < stop) {
+      const uint32_t dst = ring + slot * R::kBytes;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int id = 32 * i + lane, row = id / (D / 16), ch = id % (D / 16);
+        const int64_t src = (int64_t)min(tok + row, stop - 1) * D + 16 * ch;
+        copy16(dst + row * D + 16 * R::k_chunk(row, ch), kc + src);
+        copy16(dst + R::kRows + row * D + 16 * R::v_chunk(row, ch), vc + src);
+      }
+      if (lane < 2) copy4(dst + 2 * R::kRows + 4 * lane, (lane ? vsc : ksc) + (tok >> shift));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int tok = begin + kStep * warp, slot = 0;
+#pragma unroll
+  for (int i = 0; i + 1 < R::kSlots; ++i) fetch(tok + i * kStep * kWarps, i);  // while the queries are prepared
 
   // -- query fragments, each row scaled so that its largest element is in [2^13, 2^14)
   for (int r = warp; r < 8 * NT; r += kWarps) {
@@ -173,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
       uint4 f;
       split2(x[0], x[1], f.x, f.z);
       split2(x[2], x[3], f.y, f.w);
-      sm.q[nt][w][rg * 4 + tt] = f;
+      sm.q[nt][w][0][rg * 4 + tt] = make_uint2(f.x, f.y);
+      if constexpr (LO) sm.q[nt][w][1][rg * 4 + tt] = make_uint2(f.z, f.w);
     }
     if (lane == 0) sm.crow[r] = a.attn_scale * kLog2e * tc::pow2i(-e);
   }
@@ -204,39 +259,25 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
       for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.0f;
   float ref = 0.0f;
 
-  const uint8_t* kc = c.k_codes + (int64_t)bh * c.capacity * D;
-  const uint8_t* vc = c.v_codes + (int64_t)bh * c.capacity * D;
-  const float* ksc = c.k_scales + (int64_t)bh * c.n_blocks();
-  const float* vsc = c.v_scales + (int64_t)bh * c.n_blocks();
-  const int shift = 31 - __clz(c.block);
-
-  uint32_t kr[2][KW], vr[4][VW];
-  float ks = 0.0f, vs = 0.0f;
-  // rows behind the last one repeat it, so what a lane multiplies is always cache content
-  auto k_rows = [&](int tok) {
-    load_k<D>(kr[0], kc + (int64_t)min(tok + g, stop - 1) * D, t);
-    load_k<D>(kr[1], kc + (int64_t)min(tok + g + 8, stop - 1) * D, t);
-    ks = __ldg(ksc + (tok >> shift));
-  };
-  auto v_rows = [&](int tok) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      load_v<D>(vr[j], vc + (int64_t)min(tok + 2 * t + (j & 1) + 8 * (j >> 1), stop - 1) * D, g);
-    vs = __ldg(vsc + (tok >> shift));
-  };
-
-  int tok = begin + kStep * warp;
-  if (tok < stop) {
-    k_rows(tok);
-    v_rows(tok);
-  }
   for (; tok < stop; tok += kStep * kWarps) {
-    const int next = tok + kStep * kWarps;
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::kSlots - 2) : "memory");
+    __syncwarp();  // everyone's copies of this step have landed, and the last step's slot is read
+    {
+      const int last = slot == 0 ? R::kSlots - 1 : slot - 1;
+      fetch(tok + (R::kSlots - 1) * kStep * kWarps, last);
+    }
+    const unsigned char* now = sm.ring[warp][slot];
+    slot = slot + 1 == R::kSlots ? 0 : slot + 1;
+    const float ks_now = reinterpret_cast<const float*>(now + 2 * R::kRows)[0];
+    const float vs = reinterpret_cast<const float*>(now + 2 * R::kRows)[1];
     float s[NT][2][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[nt][0][j] = s[nt][1][j] = 0.0f;
+    uint32_t kr[2][KW];
+    load_k<D>(kr[0], now + g * D, g, t);
+    load_k<D>(kr[1], now + (g + 8) * D, g, t);
 #pragma unroll
     for (int w = 0; w < KW; ++w) {
       uint32_t f[4];
@@ -244,13 +285,14 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
       F::cvt_word(kr[1][w], f[1], f[3]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint4 q = sm.q[nt][w][lane];
-        mma(s[nt][0], f, q.x, q.y);
-        mma(s[nt][1], f, q.z, q.w);
+        const uint2 hi = sm.q[nt][w][0][lane];
+        mma(s[nt][0], f, hi.x, hi.y);
+        if constexpr (LO) {
+          const uint2 lo = sm.q[nt][w][1][lane];
+          mma(s[nt][1], f, lo.x, lo.y);
+        }
       }
     }
-    const float ks_now = ks;
-    if (next < stop) k_rows(next);
 
     if (vs > ref) {  // warp-uniform: a larger V scale becomes the reference
       const float down = ref / vs;
@@ -268,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
     for (int nt = 0; nt < NT; ++nt) {
       float x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = (s[nt][0][j] + s[nt][1][j]) * (ks_now * crow[nt][j & 1]);
+      for (int j = 0; j < 4; ++j) x[j] = (LO ? s[nt][0][j] + s[nt][1][j] : s[nt][0][j]) * (ks_now * crow[nt][j & 1]);
       if (tok + kStep > open) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -312,6 +354,9 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
       wlo[nt][0] = transpose8(l0);
       wlo[nt][1] = transpose8(l1);
     }
+    uint32_t vr[4][VW];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_v<D>(vr[j], now + R::kRows + (2 * t + (j & 1) + 8 * (j >> 1)) * D, g, t);
 #pragma unroll
     for (int w = 0; w < VW; ++w) {
       uint32_t f01[4], f23[4];  // bytes 0..3 for tokens (2t, 2t+1) and (2t+8, 2t+9)
@@ -327,8 +372,10 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         }
       }
     }
-    if (next < stop) v_rows(next);
   }
+  __syncthreads();  // (the sums take the place of the rings)
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge starts and waits for this grid
 
   // -- join the warps: sums over the lanes of a row, then over the warps
 #pragma unroll
@@ -396,13 +443,14 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
 // Joins the partials of each row of the split units: with M = max m_c, o = sum
 // 2^(m_c - M) acc_c / sum 2^(m_c - M) l_c.  W warps take a row, warp w its partials w,
 // w + W, ... with a lane on every fourth output element; their sums meet in shared memory.
-// Eight warps make a row of up to 32 partials four independent loads deep (decode: few rows);
-// with up to eight partials a row a warp of its own takes it (many rows).  The launch is the
+// With up to eight partials a row a warp of its own takes it (many rows); else 8 warps, and
+// with more than 64 partials (decode of few rows) 32, so that a warp has few rounds of four
+// independent loads.  The launch is the
 // first kernel's programmatic dependent, so its start overlaps that one's tail.
-constexpr int kMergeWarps = 8;
 template <int D, int W>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs a) {
+__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) merge_q8_kernel(Q8AttendArgs a) {
   constexpr int P = (D + 127) / 128;  // pieces of 128 elements
+  constexpr int kMergeWarps = W == 1 ? 8 : W;
   __shared__ float4 sums[kMergeWarps][P][32];
   __shared__ float2 state[kMergeWarps];
   const int lane = threadIdx.x & 31, team = (threadIdx.x >> 5) / W, warp = (threadIdx.x >> 5) % W;
@@ -495,28 +543,34 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(Q8AttendArgs
   }
 }
 
-template <typename F, int D, int NT>
+template <typename F, int D, int NT, bool LO>
 cudaError_t launch_one(const Q8AttendArgs& a, cudaStream_t stream) {
   static SmemLimitSet done;
-  constexpr int bytes = sizeof(Smem<D, NT>);
-  const cudaError_t e = ensure_smem_limit(split_kernel<F, D, NT>, bytes, done);
+  constexpr int bytes = sizeof(Smem<D, NT, LO>);
+  const cudaError_t e = ensure_smem_limit(split_kernel<F, D, NT, LO>, bytes, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.plan.items());
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, split_kernel<F, D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, split_kernel<F, D, NT, LO>, a);
+}
+
+template <typename F, int D>
+cudaError_t launch_width(const Q8AttendArgs& a, cudaStream_t stream) {
+  if (a.q_bf16)
+    return a.plan.row_tile == 16 ? launch_one<F, D, 2, false>(a, stream) : launch_one<F, D, 1, false>(a, stream);
+  return a.plan.row_tile == 16 ? launch_one<F, D, 2, true>(a, stream) : launch_one<F, D, 1, true>(a, stream);
 }
 
 template <typename F>
 cudaError_t launch_format(const Q8AttendArgs& a, cudaStream_t stream) {
-  const bool two = a.plan.row_tile == 16;
   switch (a.c.d) {
-    case 64: return two ? launch_one<F, 64, 2>(a, stream) : launch_one<F, 64, 1>(a, stream);
-    case 96: return two ? launch_one<F, 96, 2>(a, stream) : launch_one<F, 96, 1>(a, stream);
-    case 128: return two ? launch_one<F, 128, 2>(a, stream) : launch_one<F, 128, 1>(a, stream);
-    default: return two ? launch_one<F, 256, 2>(a, stream) : launch_one<F, 256, 1>(a, stream);
+    case 64: return launch_width<F, 64>(a, stream);
+    case 96: return launch_width<F, 96>(a, stream);
+    case 128: return launch_width<F, 128>(a, stream);
+    default: return launch_width<F, 256>(a, stream);
   }
 }
 
@@ -530,19 +584,19 @@ cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream) {
 
 template <int D>
 static cudaError_t merge_rows(const Q8AttendArgs& a, cudaStream_t stream) {
-  const bool few = a.plan.n_parts <= 8;
-  const int per_cta = few ? kMergeWarps : 1;
+  const int W = a.plan.n_parts <= 8 ? 1 : a.plan.n_parts <= 64 ? 8 : 32, per_cta = W == 1 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.plan.split_rows() + per_cta - 1) / per_cta));
-  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.blockDim = dim3(W == 1 ? 256 : 32 * W);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, 1>, a)
-             : cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, kMergeWarps>, a);
+  if (W == 1) return cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, 1>, a);
+  if (W == 8) return cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, 8>, a);
+  return cudaLaunchKernelEx(&cfg, merge_q8_kernel<D, 32>, a);
 }
 
 cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream) {
