@@ -54,17 +54,18 @@ tq_status check_cache(const void* k_codes, const float* k_scales, const void* v_
 
 namespace {
 
-// Chunks of the context for `units` units: the count that minimises
-// (waves of work items over the resident CTAs) x (tokens of one item + a fixed
-// cost per item, in tokens).
-void split_context(int64_t units, int64_t slots, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
+// Chunks of the context for `units` units: the count that minimises the time of the busiest
+// SM, (its work items) x (tokens of one + a fixed cost per item, in tokens).  Where an SM
+// holds several CTAs, two of them reach 95% of its bandwidth and one 60% (128K, 64/8 heads,
+// d 128: 55 us with two a SM, 59 with four and twice the partial results to join).
+void split_context(int64_t units, int per_sm, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
   int64_t best = ceil_div(max_ctx, step) * step, best_cost = -1;
   for (int64_t k = 1; units > 0 && k <= ceil_div(max_ctx, step) && k <= 1024; ++k) {
     const int64_t chunk = ceil_div(ceil_div(max_ctx, k), step) * step;
-    const int64_t items = units * ceil_div(max_ctx, chunk);
-    const int64_t cost = ceil_div(items, slots) * (chunk + item_cost);
+    const int64_t each = ceil_div(units * ceil_div(max_ctx, chunk), kSmCount);
+    const int64_t cost = each * (chunk + item_cost) * (per_sm == 1 || each > 2 ? 20 : each == 2 ? 21 : 33);
     if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk;
-    if (units * k > 4 * slots) break;
+    if (units * k > 4 * per_sm * kSmCount) break;
   }
   if (best > INT32_MAX) best = INT32_MAX / step * step;
   p->chunk = (int)best;
@@ -79,28 +80,29 @@ bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, 
   if (!q8_head_dim_supported(d)) return false;
   const int64_t G = Hq / Hkv, rows = G * n;
   if (rows > INT32_MAX / 2 || (int64_t)B * Hkv > INT32_MAX || (int64_t)B * Hq * n > INT32_MAX) return false;
-  int64_t slots, step, item_cost;
+  int per_sm;
+  int64_t step, item_cost;
   if (bf16 && rows > 16) {
     p->mode = d > 128 ? kQ8OneStream : rows > 128 ? kQ8TwoRows : kQ8TwoStreams;
     p->row_tile = p->mode == kQ8TwoRows ? 256 : 128;
     p->parts = p->mode == kQ8TwoStreams ? 2 : 1;
-    slots = kSmCount;
+    per_sm = 1;
     step = p->parts * q8_tc_tile_tokens(d);
     item_cost = 512;
   } else {
     p->mode = kQ8Warps;
     p->row_tile = rows <= 8 ? 8 : 16;
     p->parts = 1;
-    slots = q8_split_slots(d, p->row_tile);
+    per_sm = q8_split_per_sm(d, p->row_tile);
     step = 64;
-    item_cost = 256;
+    item_cost = 512;
   }
   p->tiles = (int)ceil_div(rows, p->row_tile);
   const int64_t units = (int64_t)B * Hkv * p->tiles;
   if (units > INT32_MAX) return false;
   p->units = (int)units;
-  p->whole = p->parts > 1 ? 0 : (int)(units / slots * slots);
-  split_context(units - p->whole, slots, max_ctx, step, item_cost, p);
+  p->whole = p->parts > 1 ? 0 : (int)(units / (per_sm * kSmCount) * (per_sm * kSmCount));
+  split_context(units - p->whole, per_sm, max_ctx, step, item_cost, p);
   p->n_parts = p->n_chunks * p->parts;
   if (p->n_parts == 1) p->whole = (int)units;
   p->part_stride = d + 4;

@@ -75,7 +75,7 @@ bool q8_head_dim_supported(int d);
 bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, Q8Plan* plan);
 cudaError_t launch_q8_append(const Q8WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t stream);
-int q8_split_slots(int d, int row_tile);  // work items of the split kernel resident on the GPU
+int q8_split_per_sm(int d, int row_tile);  // work items of the split kernel resident on an SM
 cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream);
 int q8_tc_tile_tokens(int d);             // tokens of one step of the tensor-memory kernel
 cudaError_t launch_q8_tc(const Q8AttendArgs& a, cudaStream_t stream);

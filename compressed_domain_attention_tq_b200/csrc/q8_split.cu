@@ -63,6 +63,10 @@ template <int D, int NT = 1>
 struct Ring {
   // as many steps as leave room for the CTAs that the registers allow (resident())
   static constexpr int kRows = kStep * D, kBytes = 2 * kRows + 16, kSlots = D == 64 ? 4 : D == 256 && NT == 2 ? 2 : 3;
+  // A step's rows are contiguous in the cache; lane l copies its chunks 32 i + l, i < D / 32.
+  // Where they go: 512 i behind chunk l's place, for V with the bits of the row that change
+  // with i folded in.
+  static __host__ __device__ constexpr int v_flip(int i) { return D == 256 ? 32 * i & 96 : D == 128 ? 64 * i & 64 : 0; }
   static __device__ __forceinline__ int k_chunk(int row, int ch) { return D >= 128 ? ch ^ ((row & 1) << 2) : ch; }
   static __device__ __forceinline__ int v_chunk(int row, int ch) {
     return D >= 128 ? ch ^ (row & 6) : D == 64 ? ch ^ (row & 2) : ch;
@@ -183,18 +187,27 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   // step `tok` into slot `slot` (rows behind the last one repeat it, so what a lane multiplies
   // is always cache content); an empty group where there is none
   const uint32_t ring = tc::smem_u32(sm.ring[warp]);
+  const int row_l = lane / (D / 16), ch_l = lane % (D / 16);
+  const uint32_t k_at = row_l * D + 16 * R::k_chunk(row_l, ch_l), v_at = row_l * D + 16 * R::v_chunk(row_l, ch_l);
   auto fetch = [&](int tok, int slot) {
-    if (tok < stop) {
-      const uint32_t dst = ring + slot * R::kBytes;
+    const uint32_t dst = ring + slot * R::kBytes;
+    if (tok + kStep <= stop) {
+      const int64_t src = (int64_t)tok * D + 16 * lane;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const int id = 32 * i + lane, row = id / (D / 16), ch = id % (D / 16);
+        copy16(dst + k_at + 512 * i, kc + src + 512 * i);
+        copy16(dst + R::kRows + (v_at ^ R::v_flip(i)) + 512 * i, vc + src + 512 * i);
+      }
+    } else if (tok < stop) {
+#pragma unroll 1
+      for (int id = lane; id < D; id += 32) {
+        const int row = id / (D / 16), ch = id % (D / 16);
         const int64_t src = (int64_t)min(tok + row, stop - 1) * D + 16 * ch;
         copy16(dst + row * D + 16 * R::k_chunk(row, ch), kc + src);
         copy16(dst + R::kRows + row * D + 16 * R::v_chunk(row, ch), vc + src);
       }
-      if (lane < 2) copy4(dst + 2 * R::kRows + 4 * lane, (lane ? vsc : ksc) + (tok >> shift));
     }
+    if (tok < stop && lane < 2) copy4(dst + 2 * R::kRows + 4 * lane, (lane ? vsc : ksc) + (tok >> shift));
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int tok = begin + kStep * warp, slot = 0;
@@ -576,7 +589,7 @@ cudaError_t launch_format(const Q8AttendArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int q8_split_slots(int d, int row_tile) { return kSmCount * resident(d, row_tile / 8); }
+int q8_split_per_sm(int d, int row_tile) { return resident(d, row_tile / 8); }
 
 cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream) {
   return a.c.e4m3 ? launch_format<E4m3>(a, stream) : launch_format<Int8>(a, stream);
