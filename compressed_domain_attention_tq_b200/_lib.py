@@ -131,7 +131,7 @@ def load() -> ctypes.CDLL:
     lib.tq_quantize_append_q8.argtypes = [P, P, i32, i32, i32, i32, i32, i32, i32, P, P, P, P, P, P,
                                           i64, P]
     lib.tq_quantize_append_q8.restype = i32
-    lib.tq_read_q8.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, i32, P, P, i32, P, P, i32, P]
+    lib.tq_read_q8.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, i32, P, P, i32, P, P, i32, i32, P]
     lib.tq_read_q8.restype = i32
     lib.tq_sdpa_q8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.tq_sdpa_q8_workspace_bytes.restype = sz
@@ -730,16 +730,13 @@ def read_q8(k_codes, k_scales, v_codes, v_scales, block, pos, rows, n_valid=None
     _q8_lens(B, pos=pos, n_valid=n_valid)
     with _Launch(device, stream) as s:
         if out is None:
-            # without pos and n_valid every row inside the cache is written
-            whole = pos is None and n_valid is None and rows <= cap
-            make = torch.empty if whole else torch.zeros
-            ko = make(B, H, rows, d, dtype=dtype, device=device)
-            vo = make(B, H, rows, d, dtype=dtype, device=device)
+            ko = torch.empty((B, H, rows, d), dtype=dtype, device=device)
+            vo = torch.empty((B, H, rows, d), dtype=dtype, device=device)
         elif ko.shape != (B, H, rows, d) or vo.shape != ko.shape or ko.dtype != vo.dtype:
             raise ValueError("out must be two tensors [B][Hkv][rows][d] of one dtype")
         rc = load().tq_read_q8(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                v_scales.data_ptr(), cap, B, H, d, fmt, block, _ptr(pos), _ptr(n_valid),
-                               rows, ko.data_ptr(), vo.data_ptr(), _dtype_of(ko.dtype), s)
+                               rows, ko.data_ptr(), vo.data_ptr(), _dtype_of(ko.dtype), out is None, s)
     if rc != TQ_OK:
         raise TQError(rc, "tq_read_q8")
     return ko, vo

@@ -190,7 +190,7 @@ tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_c
                      const float* v_scales, int64_t capacity, int32_t batch, int32_t num_kv_heads,
                      int32_t head_dim, tq_q8_format format, int32_t block, const int32_t* pos,
                      const int32_t* n_valid, int32_t rows, void* k_out, void* v_out,
-                     tq_dtype out_dtype, void* cuda_stream) {
+                     tq_dtype out_dtype, int32_t fill, void* cuda_stream) {
   Q8ReadArgs a = {};
   const tq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, capacity, batch, num_kv_heads,
                                    head_dim, format, block, &a.c);
@@ -206,6 +206,7 @@ tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_c
   a.n = rows;
   a.pos = pos;
   a.n_valid = n_valid;
+  a.fill = fill != 0;
   return status_of(launch_q8_read(a, static_cast<cudaStream_t>(cuda_stream)), "tq_read_q8");
 }
 

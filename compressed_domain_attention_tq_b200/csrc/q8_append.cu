@@ -1,8 +1,8 @@
 // q8_append.cu -- writing tokens into the 8-bit block-scaled cache, and
 // reading a range of it back.
 //
-// Writing.  One CTA owns one block of one kv head's K or V, so the block's new
-// scale and every code that changes with it are decided in one place:
+// Writing.  One team of threads owns one block of one kv head's K or V, so the block's
+// new scale and every code that changes with it are decided in one place:
 //   a     = max finite |x| over the block's new rows,  s_new = fl32(a / Q)
 //   s     = max(s_old, s_new) if rows of the block before the first new one are
 //           kept, else s_new
@@ -10,8 +10,10 @@
 //   kept rows, only when s > s_old:  code' = R(fl32(fl32(code s_old) / s))
 // The new rows stay in registers between the maximum and the division, so HBM
 // sees each input once and each code once.  A thread holds four pieces of
-// eight elements (one 16-byte load of bf16, one 8-byte store), which makes the
-// CTA block * d / 32 threads (32 to 1024).  Bound: HBM.
+// eight elements (one 16-byte load of bf16, one 8-byte store), six at d = 96, which
+// makes a team of 32 to 1024 threads; small teams share a CTA of 256.  Bound: HBM
+// for fp32 inputs, nearly the instructions for bf16 (the exact division is five
+// packed operations a pair, half of it all).
 //
 // Reading is a stream of 8-byte (bf16) or 4-byte (fp32) code loads with one
 // 16-byte store each.  Bound: HBM.
@@ -23,7 +25,6 @@ namespace {
 
 using namespace q8;
 
-constexpr int kPieces = 4;  // pieces of 8 elements per thread
 
 template <bool BF16>
 struct Piece {
@@ -41,46 +42,75 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
+  __device__ __forceinline__ void values(float2 (&x)[4]) const {
     if constexpr (BF16) {
       const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
+      for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
     } else {
       const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+      for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+    }
+  }
+  // Running maximum of the bits of |x|: two 16-bit lanes for bf16, one word for fp32.
+  __device__ __forceinline__ void max_bits(uint32_t& top) const {
+    if constexpr (BF16) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(u[i] & 0x7fff7fffu));
+    } else {
+      const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) top = __vimax3_u32(top, u[i] & 0x7fffffffu, u[i + 1] & 0x7fffffffu);
     }
   }
 };
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* smem) {
+// Maximum over the `threads` threads (whole warps) of one block's team; smem[32] is the
+// CTA's, and each team has a barrier of its own.
+__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* smem, int threads, int team) {
   v = __reduce_max_sync(0xffffffffu, v);
-  const int warps = blockDim.x >> 5;
+  const int warps = threads >> 5, lane = threadIdx.x & 31;
   if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = (threadIdx.x & 31) < warps ? smem[threadIdx.x & 31] : 0u;
+  if (lane == 0) smem[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(threads) : "memory");
+  v = lane < warps ? smem[team * warps + lane] : 0u;
   return __reduce_max_sync(0xffffffffu, v);
 }
 
-template <typename F, bool BF16>
-__global__ void __launch_bounds__(1024) append_kernel(Q8WriteArgs a, int touched) {
+// x / d for x, d < 2^31 by the upper half of x ceil(2^64 / d) (the error, below x d / 2^64,
+// does not reach the next integer); integer division took a third of a team's instructions.
+struct Quotient {
+  uint64_t m;
+  explicit Quotient(unsigned d) : m(~0ull / d + 1) {}  // 0 for d = 1
+  __device__ __forceinline__ unsigned of(unsigned x) const { return m ? (unsigned)__umul64hi(x, m) : x; }
+};
+
+struct Teams {
+  int touched;   // blocks of one sequence's window
+  int shift;     // log2 of a team's threads
+  unsigned units;
+  Quotient per_head, per_sequence;
+};
+
+template <typename F, bool BF16, int kPieces>
+__global__ void __launch_bounds__(1024, BF16 ? 1 : 0) append_kernel(Q8WriteArgs a, Teams teams) {
   __shared__ uint32_t red[2][32];
   const Q8Cache& c = a.c;
-  const bool is_v = blockIdx.x & 1;
-  const unsigned unit = blockIdx.x >> 1;
-  const int j = unit % touched;  // block of this sequence's window
-  const int bh = unit / touched;
-  const int b = bh / c.Hkv;
+  const int threads = 1 << teams.shift, team = threadIdx.x >> teams.shift, tid = threadIdx.x & (threads - 1);
+  const unsigned id = blockIdx.x * (blockDim.x >> teams.shift) + team;
+  if (id >= teams.units) return;
+  const bool is_v = id & 1;
+  const int bh = teams.per_head.of(id >> 1);
+  const int j = (id >> 1) - bh * teams.touched;  // block of this sequence's window
+  const int b = teams.per_sequence.of(bh);
+  const int block_shift = 31 - __clz(c.block);
   int pos = a.pos[b], valid = a.n_valid ? a.n_valid[b] : a.n;
   if (a.pos_is_ctx) pos = min(pos, a.max_ctx) - 1;
   if (pos < 0 || valid <= 0) return;
   valid = min(valid, a.n);
-  const int64_t first = (int64_t)(pos / c.block + j) * c.block;  // the block's first row
+  const int64_t first = (int64_t)((pos >> block_shift) + j) << block_shift;  // the block's first row
   const int64_t stop = min((int64_t)pos + valid, c.capacity);
   const int new0 = (int)max((int64_t)0, pos - first);           // new rows [new0, new1) of the block
   const int new1 = (int)min((int64_t)c.block, stop - first);
@@ -89,7 +119,7 @@ __global__ void __launch_bounds__(1024) append_kernel(Q8WriteArgs a, int touched
   const int per_row = c.d >> 3;
   const void* in = is_v ? a.v : a.k;
   uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + ((int64_t)bh * c.capacity + first) * c.d;
-  float* scale = (is_v ? c.v_scales : c.k_scales) + (int64_t)bh * c.n_blocks() + first / c.block;
+  float* scale = (is_v ? c.v_scales : c.k_scales) + (int64_t)bh * ((c.capacity + c.block - 1) >> block_shift) + (first >> block_shift);
   // element of the input that corresponds to the block's row 0
   const int64_t in0 = ((int64_t)bh * a.n + (first - pos)) * c.d;
   const float s_old = new0 > 0 ? *scale : 0.0f;
@@ -97,36 +127,33 @@ __global__ void __launch_bounds__(1024) append_kernel(Q8WriteArgs a, int touched
   Piece<BF16> x[kPieces];
   uint32_t top = 0;  // bits of the largest |x|: above 0x7f800000 for NaN
   const int lo = new0 * per_row, hi = new1 * per_row;
+  const bool whole = lo == 0 && hi == kPieces * threads;  // (no piece to leave out)
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int p = threadIdx.x + i * blockDim.x;
-    if (p >= lo && p < hi)
+    const int p = tid + i * threads;
+    if (whole || (p >= lo && p < hi))
       x[i].load(in, in0 + (int64_t)p * 8);
     else
       x[i].zero();
   }
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    float v[8];
-    x[i].values(v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-  }
-  top = block_max(top, red[0]);
+  for (int i = 0; i < kPieces; ++i) x[i].max_bits(top);
+  if constexpr (BF16) top = max(top << 16, top & 0xffff0000u);
+  top = team_max(top, red[0], threads, team);
   const bool finite = top < 0x7f800000u;
   if (!finite) {  // infinities and NaN do not set the scale
     top = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      float v[8];
+      float2 v[4];
       x[i].values(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t u = __float_as_uint(v[e]) & 0x7fffffffu;
+        const uint32_t u = __float_as_uint(e & 1 ? v[e >> 1].y : v[e >> 1].x) & 0x7fffffffu;
         if (u < 0x7f800000u) top = max(top, u);
       }
     }
-    top = block_max(top, red[1]);
+    top = team_max(top, red[1], threads, team);
   }
   const float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(top), F::kMax));
   const Divider div = Divider::by(s);
@@ -134,32 +161,31 @@ __global__ void __launch_bounds__(1024) append_kernel(Q8WriteArgs a, int touched
   if (finite && div.fast) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * blockDim.x;
-      float v[8];
+      const int p = tid + i * threads;
+      float2 v[4];
       x[i].values(v);
-      float y[2][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = div.quick(v[e]);
-      if (p >= lo && p < hi)
-        *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = make_uint2(F::codes4(y[0]), F::codes4(y[1]));
+      for (int e = 0; e < 4; ++e) v[e] = div.quick(v[e]);
+      if (whole || (p >= lo && p < hi))
+        *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = make_uint2(F::codes4(v[0], v[1]), F::codes4(v[2], v[3]));
     }
   } else {
 #pragma unroll 1
     for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * blockDim.x;
+      const int p = tid + i * threads;
       if (p < lo || p >= hi) continue;
       Piece<BF16> again;  // re-read: a block with such values is rare
       again.load(in, in0 + (int64_t)p * 8);
-      float v[8];
+      float2 v[4];
       again.values(v);
       uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= F::code(div.any(v[e])) << (8 * (e & 3));
+      for (int e = 0; e < 8; ++e) w[e >> 2] |= F::code(div.any(e & 1 ? v[e >> 1].y : v[e >> 1].x)) << (8 * (e & 3));
       *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = make_uint2(w[0], w[1]);
     }
   }
   if (new0 > 0 && s > s_old) {  // the kept rows' codes move to the larger scale
-    for (int p = threadIdx.x; p < lo; p += blockDim.x) {
+    for (int p = tid; p < lo; p += threads) {
       uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)p * 8);
       const uint2 old = *at;
       uint32_t w[2] = {0, 0};
@@ -169,7 +195,7 @@ __global__ void __launch_bounds__(1024) append_kernel(Q8WriteArgs a, int touched
       *at = make_uint2(w[0], w[1]);
     }
   }
-  if (threadIdx.x == 0) *scale = s;
+  if (tid == 0) *scale = s;
 }
 
 // -------------------------------------------------------------------- reading
@@ -185,11 +211,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(Q8ReadArgs a, int ro
   const unsigned unit = blockIdx.x >> 1;
   const int tile = unit % row_tiles, bh = unit / row_tiles, b = bh / c.Hkv;
   const int pos = a.pos ? a.pos[b] : 0;
-  if (pos < 0) return;
-  const int row0 = tile * tile_rows;
+  const int row0 = tile * tile_rows, all = min(tile_rows, a.n - row0);
   int64_t rows = min(a.n_valid ? a.n_valid[b] : a.n, a.n);
-  rows = min(min(rows, c.capacity - pos) - row0, (int64_t)tile_rows);
-  if (rows <= 0) return;
+  rows = min(min(rows, c.capacity - pos) - row0, (int64_t)all);
+  if (rows <= 0 || pos < 0) rows = 0;
   constexpr int E = BF16 ? 8 : 4;
   const int per_row = c.d / E, pieces = (int)rows * per_row;
   const uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + ((int64_t)bh * c.capacity + pos + row0) * c.d;
@@ -197,6 +222,9 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(Q8ReadArgs a, int ro
   unsigned char* out = static_cast<unsigned char*>(is_v ? a.v : a.k) +
                        ((int64_t)bh * a.n + row0) * c.d * (BF16 ? 2 : 4);
   const int first = pos + row0;
+  if (a.fill)  // rows outside the cache or behind the last are zeros
+    for (int p = pieces + threadIdx.x; p < all * per_row; p += kReadThreads)
+      __stcs(reinterpret_cast<uint4*>(out) + p, make_uint4(0, 0, 0, 0));
   for (int p0 = threadIdx.x; p0 < pieces; p0 += kReadThreads * kReadPieces) {
     uint32_t w[kReadPieces][2];
     float s[kReadPieces];
@@ -236,14 +264,21 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(Q8ReadArgs a, int ro
 
 }  // namespace
 
+template <int kPieces>
+static cudaError_t write_blocks(const Q8WriteArgs& a, int touched, unsigned units, cudaStream_t stream) {
+  const int threads = a.c.block * a.c.d / (8 * kPieces), cta = threads > 256 ? threads : 256;
+  const Teams teams = {touched, 31 - __builtin_clz((unsigned)threads), units, Quotient(touched), Quotient(a.c.Hkv)};
+  const unsigned per_cta = cta / threads;
+  auto* kernel = a.c.e4m3 ? (a.bf16 ? append_kernel<E4m3, true, kPieces> : append_kernel<E4m3, false, kPieces>)
+                          : (a.bf16 ? append_kernel<Int8, true, kPieces> : append_kernel<Int8, false, kPieces>);
+  kernel<<<(units + per_cta - 1) / per_cta, cta, 0, stream>>>(a, teams);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_q8_append(const Q8WriteArgs& a, cudaStream_t stream) {
   const int touched = (a.n + a.c.block - 2) / a.c.block + 1;  // most blocks n rows can lie in
-  const unsigned grid = 2u * a.c.B * a.c.Hkv * touched;
-  const int threads = (a.c.block * a.c.d / (8 * kPieces) + 31) / 32 * 32;
-  auto* kernel = a.c.e4m3 ? (a.bf16 ? append_kernel<E4m3, true> : append_kernel<E4m3, false>)
-                          : (a.bf16 ? append_kernel<Int8, true> : append_kernel<Int8, false>);
-  kernel<<<grid, threads, 0, stream>>>(a, touched);
-  return cudaGetLastError();
+  const unsigned units = 2u * a.c.B * a.c.Hkv * touched;
+  return a.c.d == 96 ? write_blocks<6>(a, touched, units, stream) : write_blocks<4>(a, touched, units, stream);
 }
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t stream) {

@@ -19,6 +19,32 @@ namespace q8 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// two fp32 operations of one instruction, each rounded to nearest
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 struct Int8 {
   static constexpr float kMax = 127.0f;
   // byte place of a 32-bit word that cvt_word puts into half k of pair p
@@ -49,11 +75,12 @@ struct Int8 {
     return (uint32_t)__float2int_rn(y) & 0xffu;
   }
   // four finite y with |y| <= kMax + 1/2: halves to even by the fp32 adder
-  static __device__ __forceinline__ uint32_t codes4(const float (&y)[4]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(y[i] + 12582912.0f);  // 1.5 * 2^23
-    return tc::prmt(tc::prmt(u[0], u[1], 0x0040), tc::prmt(u[2], u[3], 0x0040), 0x5410);
+  static __device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
+    const float2 magic = make_float2(12582912.0f, 12582912.0f);  // 1.5 * 2^23
+    a = add2(a, magic);
+    b = add2(b, magic);
+    return tc::prmt(tc::prmt(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                    tc::prmt(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
   }
 };
 
@@ -91,8 +118,8 @@ struct E4m3 {
   static __device__ __forceinline__ uint32_t code(float y) {
     return pack2(y != y ? 0.0f : fminf(fmaxf(y, -kMax), kMax), 0.0f) & 0xffu;
   }
-  static __device__ __forceinline__ uint32_t codes4(const float (&y)[4]) {
-    return pack2(y[0], y[1]) | (pack2(y[2], y[3]) << 16);
+  static __device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
+    return pack2(a.x, a.y) | (pack2(b.x, b.y) << 16);
   }
 };
 
@@ -118,10 +145,11 @@ struct Divider {
   static __device__ __forceinline__ Divider by(float s) {
     return {s, __frcp_rn(s), s >= 0x1p-90f && s <= 0x1p100f};
   }
-  __device__ __forceinline__ float quick(float x) const {
-    float q = x * r;
-    q = fmaf(fmaf(-q, s, x), r, q);
-    return fmaf(fmaf(-q, s, x), r, q);
+  __device__ __forceinline__ float2 quick(float2 x) const {  // (x - q s as fma(q, -s, x), which is exact too)
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
+    float2 q = mul2(x, r2);
+    q = fma2(fma2(q, s2, x), r2, q);
+    return fma2(fma2(q, s2, x), r2, q);
   }
   __device__ __forceinline__ float any(float x) const { return s > 0.0f ? __fdiv_rn(x, s) : 0.0f; }
 };

@@ -30,6 +30,7 @@ struct Q8ReadArgs {
   void *k, *v;  // [B][Hkv][n][d]
   int bf16, n;
   const int32_t *pos, *n_valid;
+  int fill;
 };
 
 // The kernel of an attention call, and what a CTA of the tensor-memory one holds

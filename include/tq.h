@@ -579,15 +579,17 @@ TQ_API tq_status tq_quantize_append_q8(
  * (fp32: fl32(scale * code); bf16: that rounded once).
  *  pos       device int32 [B], or NULL for 0.
  *  n_valid   device int32 [B] or NULL: only the first n_valid[b] rows.
- * Outputs of rows outside the cache (pos[b] + i >= capacity, pos[b] < 0) or at
- * n_valid[b] and behind are left as they were.  Errors as tq_quantize_append_q8.
+ *  fill      0: outputs of rows outside the cache (pos[b] + i >= capacity,
+ *            pos[b] < 0) or at n_valid[b] and behind are left as they were;
+ *            else they become zeros.
+ * Errors as tq_quantize_append_q8.
  */
 TQ_API tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_codes,
                             const float* v_scales, int64_t capacity, int32_t batch,
                             int32_t num_kv_heads, int32_t head_dim, tq_q8_format format,
                             int32_t block, const int32_t* pos, const int32_t* n_valid,
                             int32_t rows, void* k_out, void* v_out, tq_dtype out_dtype,
-                            void* cuda_stream);
+                            int32_t fill, void* cuda_stream);
 
 /* Bytes of device workspace tq_sdpa_q8 needs for these sizes (host only); 0
  * for invalid sizes.  tq_sdpa_q8_decode_append needs those of n_q = 1. */

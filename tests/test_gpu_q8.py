@@ -157,6 +157,23 @@ def test_append_skips_what_it_should():
         assert torch.all(ko[b, :, m:] == 7.0)
 
 
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_read_without_out_is_zero_outside(dtype):
+    """Rows at n_valid and behind, outside the cache, and of sequences with a negative row."""
+    ref, c = pair(4, 2, 150, 96, 32, "e4m3")
+    x = randn((4, 2, 150, 96), 8, BF16)
+    ref.append(f64(x), f64(-x), [0] * 4)
+    c.append(x.cuda(), -x.cuda(), i32([0] * 4))
+    torch.full((4, 2, 70, 96), 7.0, device="cuda", dtype=dtype)  # (memory that the outputs may get again)
+    got = c.read(i32([-1, 100, 31, 2 ** 31 - 1]), 70, n_valid=i32([70, 70, 33, 70]), dtype=dtype)
+    for w, y in enumerate(got):
+        for b, (at, m) in enumerate([(0, 0), (100, 50), (31, 33), (0, 0)]):
+            for h in range(2):
+                want = torch.from_numpy(ref.values(w, b, h, at, at + m)).float().to(dtype)
+                assert torch.equal(y[b, h, :m].cpu(), want) and torch.all(y[b, h, m:] == 0)
+
+
 # ------------------------------------------------------------------------ attention
 
 CASES = [  # d, block, H, G, n, ctx, q_lens

@@ -27,7 +27,7 @@ def call(lib, what, **kw):
                                          a["block"], a["pos"], a["valid"], *cache, a["cap"], None)
     if what == "read":
         return lib.tq_read_q8(*cache, a["cap"], a["B"], a["Hkv"], a["d"], a["fmt"], a["block"], a["pos"],
-                              a["valid"], a["n"], a["k"], a["v"], a["out_dtype"], None)
+                              a["valid"], a["n"], a["k"], a["v"], a["out_dtype"], 0, None)
     if what == "attend":
         return lib.tq_sdpa_q8(a["q"], a["dtype"], a["B"], a["Hq"], a["Hkv"], a["n"], a["d"], a["fmt"],
                               a["block"], *cache, a["cap"], a["pos"], a["valid"], a["max_ctx"], a["scale"],
