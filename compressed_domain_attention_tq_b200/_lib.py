@@ -7,6 +7,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -675,29 +676,47 @@ def _q8_lens(B, **lens):
             raise ValueError(f"{name} must be int32 [B]")
 
 
-class _Launch:
-    """The device and stream a q8 call runs on: the tensors' device, and there the
-    given stream or the current one.  Buffers a call allocates belong to that stream."""
+class _Here:
+    """The current stream of the current device: nothing to switch to."""
 
-    __slots__ = ("device", "stream", "_ctx")
+    __slots__ = ("raw",)
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        pass
+
+
+class _There:
+    """A given stream, or the current one of a device that is not the current one; buffers
+    a call allocates inside belong to it."""
+
+    __slots__ = ("stream", "_ctx")
 
     def __init__(self, device, stream):
-        self.device = device
         self.stream = torch.cuda.current_stream(device) if stream is None else stream
         if self.stream.device != device:
             raise ValueError("the stream belongs to another device than the tensors")
-        self._ctx = None
-        if stream is not None or device.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.stream(self.stream)
+        self._ctx = torch.cuda.stream(self.stream)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        self._ctx.__enter__()
+        return self.stream.cuda_stream
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        self._ctx.__exit__(*exc)
+
+
+def _launch(device, stream):
+    """The device and stream a q8 call runs on: the tensors' device, and there the given
+    stream or the current one."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
+    return _There(device, stream)
 
 
 def quantize_append_q8(k, v, pos, k_codes, k_scales, v_codes, v_scales, block, n_valid=None,
@@ -711,7 +730,7 @@ def quantize_append_q8(k, v, pos, k_codes, k_scales, v_codes, v_scales, block, n
     if k.dtype != v.dtype:
         raise TypeError("k and v must share dtype")
     _q8_lens(B, pos=pos, n_valid=n_valid)
-    with _Launch(device, stream) as s:
+    with _launch(device, stream) as s:
         rc = load().tq_quantize_append_q8(k.data_ptr(), v.data_ptr(), _dtype_of(k.dtype), B, H, k.shape[2],
                                           d, fmt, block, pos.data_ptr(), _ptr(n_valid), k_codes.data_ptr(),
                                           k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
@@ -728,10 +747,9 @@ def read_q8(k_codes, k_scales, v_codes, v_scales, block, pos, rows, n_valid=None
     ko, vo = (None, None) if out is None else out
     device, B, H, cap, d, fmt = _q8_check(k_codes, k_scales, v_codes, v_scales, block, pos, n_valid, ko, vo)
     _q8_lens(B, pos=pos, n_valid=n_valid)
-    with _Launch(device, stream) as s:
+    with _launch(device, stream) as s:
         if out is None:
-            ko = torch.empty((B, H, rows, d), dtype=dtype, device=device)
-            vo = torch.empty((B, H, rows, d), dtype=dtype, device=device)
+            ko, vo = (k_scales.new_empty((B, H, rows, d), dtype=dtype) for _ in range(2))
         elif ko.shape != (B, H, rows, d) or vo.shape != ko.shape or ko.dtype != vo.dtype:
             raise ValueError("out must be two tensors [B][Hkv][rows][d] of one dtype")
         rc = load().tq_read_q8(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
@@ -748,19 +766,24 @@ def sdpa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, n_q, max
                                                  _dtype_of(dtype)))
 
 
-def _q8_workspace(workspace, B, Hq, H, d, n, max_ctx, out_code, device):
+@functools.lru_cache(maxsize=1024)
+def _q8_workspace_bytes(B, Hq, H, d, n, max_ctx, out_code):
+    return load().tq_sdpa_q8_workspace_bytes(B, Hq, H, d, n, max_ctx, out_code)
+
+
+def _q8_workspace(workspace, q, B, Hq, H, d, n, max_ctx, out_code):
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    need = load().tq_sdpa_q8_workspace_bytes(B, Hq, H, d, n, max_ctx, out_code)
-    return torch.empty(max(need, 16), dtype=torch.uint8, device=device), need
+    need = _q8_workspace_bytes(B, Hq, H, d, n, max_ctx, out_code)
+    return q.new_empty(max(need, 16), dtype=torch.uint8), need
 
 
-def _q8_out(out, lse, shape, dtype, device, make):
+def _q8_out(out, lse, q, dtype, zero=False):
     if out is None:
-        out = make(shape, dtype=dtype, device=device)
-    elif out.shape != shape:
+        out = (torch.zeros_like if zero else torch.empty_like)(q, dtype=dtype)
+    elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (*shape[:-1], 2)):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (*q.shape[:-1], 2)):
         raise ValueError("lse must be float32, the shape of q with 2 in the place of d")
     return out
 
@@ -778,10 +801,10 @@ def sdpa_q8(q, k_codes, k_scales, v_codes, v_scales, block, ctx_lens, max_ctx, q
         raise ValueError("q must be [B][Hq][n][d]")
     _q8_lens(B, ctx_lens=ctx_lens, q_lens=q_lens)
     Hq, n = q.shape[1], q.shape[2]
-    with _Launch(device, stream) as s:
-        out = _q8_out(out, lse, q.shape, q.dtype, device, torch.empty if q_lens is None else torch.zeros)
+    with _launch(device, stream) as s:
+        out = _q8_out(out, lse, q, q.dtype, zero=q_lens is not None)
         code = _dtype_of(out.dtype)
-        workspace, ws_bytes = _q8_workspace(workspace, B, Hq, H, d, n, max_ctx, code, device)
+        workspace, ws_bytes = _q8_workspace(workspace, q, B, Hq, H, d, n, max_ctx, code)
         rc = load().tq_sdpa_q8(q.data_ptr(), _dtype_of(q.dtype), B, Hq, H, n, d, fmt, block,
                                k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                v_scales.data_ptr(), cap, ctx_lens.data_ptr(), _ptr(q_lens), max_ctx,
@@ -802,10 +825,10 @@ def sdpa_q8_decode(q, k_codes, k_scales, v_codes, v_scales, block, ctx_lens, max
         raise ValueError("q must be [B][Hq][d]")
     _q8_lens(B, ctx_lens=ctx_lens)
     Hq = q.shape[1]
-    with _Launch(device, stream) as s:
-        out = _q8_out(out, lse, q.shape, torch.float32, device, torch.empty)
+    with _launch(device, stream) as s:
+        out = _q8_out(out, lse, q, torch.float32)
         code = _dtype_of(out.dtype)
-        workspace, ws_bytes = _q8_workspace(workspace, B, Hq, H, d, 1, max_ctx, code, device)
+        workspace, ws_bytes = _q8_workspace(workspace, q, B, Hq, H, d, 1, max_ctx, code)
         rc = load().tq_sdpa_q8(q.data_ptr(), _dtype_of(q.dtype), B, Hq, H, 1, d, fmt, block,
                                k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                v_scales.data_ptr(), cap, ctx_lens.data_ptr(), None, max_ctx,
@@ -830,10 +853,10 @@ def sdpa_q8_decode_append(q, k_new, v_new, k_codes, k_scales, v_codes, v_scales,
         raise TypeError("k_new and v_new must share dtype")
     _q8_lens(B, ctx_lens=ctx_lens)
     Hq = q.shape[1]
-    with _Launch(device, stream) as s:
-        out = _q8_out(out, lse, q.shape, torch.float32, device, torch.empty)
+    with _launch(device, stream) as s:
+        out = _q8_out(out, lse, q, torch.float32)
         code = _dtype_of(out.dtype)
-        workspace, ws_bytes = _q8_workspace(workspace, B, Hq, H, d, 1, max_ctx, code, device)
+        workspace, ws_bytes = _q8_workspace(workspace, q, B, Hq, H, d, 1, max_ctx, code)
         rc = load().tq_sdpa_q8_decode_append(
             q.data_ptr(), _dtype_of(q.dtype), k_new.data_ptr(), v_new.data_ptr(), _dtype_of(k_new.dtype),
             B, Hq, H, d, fmt, block, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),

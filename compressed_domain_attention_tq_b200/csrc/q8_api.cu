@@ -60,12 +60,14 @@ namespace {
 // d 128: 55 us with two a SM, 59 with four and twice the partial results to join).
 void split_context(int64_t units, int per_sm, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
   int64_t best = ceil_div(max_ctx, step) * step, best_cost = -1;
-  for (int64_t k = 1; units > 0 && k <= ceil_div(max_ctx, step) && k <= 1024; ++k) {
-    const int64_t chunk = ceil_div(ceil_div(max_ctx, k), step) * step;
+  // the most chunks with which no SM has more than `most` items
+  const int64_t least = ceil_div(units, kSmCount);
+  for (int64_t most = least; units > 0 && most <= (least > 4 * per_sm ? least : 4 * per_sm); ++most) {
+    const int64_t k = most * kSmCount / units;  // >= 1
+    const int64_t chunk = ceil_div(ceil_div(max_ctx, k < 1024 ? k : 1024), step) * step;
     const int64_t each = ceil_div(units * ceil_div(max_ctx, chunk), kSmCount);
     const int64_t cost = each * (chunk + item_cost) * (per_sm == 1 || each > 2 ? 20 : each == 2 ? 21 : 33);
     if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk;
-    if (units * k > 4 * per_sm * kSmCount) break;
   }
   if (best > INT32_MAX) best = INT32_MAX / step * step;
   p->chunk = (int)best;
