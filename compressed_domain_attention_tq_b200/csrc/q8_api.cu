@@ -58,8 +58,9 @@ namespace {
 // SM, (its work items) x (tokens of one + a fixed cost per item, in tokens).  Where an SM
 // holds several CTAs, two of them reach 95% of its bandwidth and one 60% (128K, 64/8 heads,
 // d 128: 55 us with two a SM, 59 with four and twice the partial results to join).
-void split_context(int64_t units, int per_sm, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
-  int64_t best = ceil_div(max_ctx, step) * step, best_cost = -1;
+// Returns the items of an SM.
+int64_t split_context(int64_t units, int per_sm, int max_ctx, int64_t step, int64_t item_cost, Q8Plan* p) {
+  int64_t items = 0, best = ceil_div(max_ctx, step) * step, best_cost = -1;
   // the most chunks with which no SM has more than `most` items
   const int64_t least = ceil_div(units, kSmCount);
   for (int64_t most = least; units > 0 && most <= (least > 4 * per_sm ? least : 4 * per_sm); ++most) {
@@ -67,11 +68,12 @@ void split_context(int64_t units, int per_sm, int max_ctx, int64_t step, int64_t
     const int64_t chunk = ceil_div(ceil_div(max_ctx, k < 1024 ? k : 1024), step) * step;
     const int64_t each = ceil_div(units * ceil_div(max_ctx, chunk), kSmCount);
     const int64_t cost = each * (chunk + item_cost) * (per_sm == 1 || each > 2 ? 20 : each == 2 ? 21 : 33);
-    if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk;
+    if (best_cost < 0 || cost < best_cost) best_cost = cost, best = chunk, items = each;
   }
   if (best > INT32_MAX) best = INT32_MAX / step * step;
   p->chunk = (int)best;
   p->n_chunks = (int)ceil_div(max_ctx, best);
+  return items;
 }
 
 }  // namespace
@@ -104,12 +106,24 @@ bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, 
   if (units > INT32_MAX) return false;
   p->units = (int)units;
   p->whole = p->parts > 1 ? 0 : (int)(units / (per_sm * kSmCount) * (per_sm * kSmCount));
-  split_context(units - p->whole, per_sm, max_ctx, step, item_cost, p);
-  p->n_parts = p->n_chunks * p->parts;
-  if (p->n_parts == 1) p->whole = (int)units;
+  const int64_t each = split_context(units - p->whole, per_sm, max_ctx, step, item_cost, p);
+  p->target = 0;
+  p->step_shift = 31 - __builtin_clz((unsigned)step);
+  if (p->n_chunks * p->parts == 1) {
+    p->whole = (int)units;
+  } else if (p->whole == 0 && B > 1 && B <= 32) {
+    // as many items as the busiest SM has, but the same number for each kv head and tile
+    const int64_t heads = (int64_t)Hkv * p->tiles;
+    p->target = (int)(each * kSmCount / heads * heads);
+    if (p->target < units) p->target = (int)units;
+    p->per_head = (int)(p->target / heads);
+  }
+  p->row_parts = p->n_chunks * p->parts;
   p->part_stride = d + 4;
   p->header_bytes = (size_t)ceil_div(4LL * B, 256) * 256;
-  p->ws_bytes = p->header_bytes + sizeof(float) * (size_t)p->split_rows() * p->n_parts * p->part_stride;
+  p->ws_bytes = p->header_bytes;
+  if (p->whole < p->units)
+    p->ws_bytes += sizeof(float) * (size_t)p->split_items() * p->row_tile * p->parts * p->part_stride;
   return p->items() <= INT32_MAX && p->split_rows() <= INT32_MAX;
 }
 

@@ -167,15 +167,15 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   const int bh = it.bh, b = it.b, hk = it.hk, G = it.G, rows = it.rows, row0 = it.row0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // a decode step's append comes first
   const Q8Seq seq(a, b);
-  if (it.chunk_id == 0 && it.tile == 0 && hk == 0 && threadIdx.x == 0)
-    static_cast<int32_t*>(a.workspace)[b] = seq.bad;
+  q8_write_flags(a);
+  if (!it.any) return;
 
   const int last_i = min(rows - 1, row0 + 8 * NT - 1) / G;  // the tile's last and first query token
   const int first_i = row0 / G;
   const int q_last = min(last_i, seq.q_len - 1);
   const int stop_all = q_last < first_i ? 0 : seq.limit(q_last);  // rows any of the tile's queries sees
-  const int begin = it.chunk_id * a.plan.chunk;
-  const int stop = it.split ? min(stop_all, begin + a.plan.chunk) : stop_all;
+  const int begin = it.chunk_id * it.chunk;
+  const int stop = it.split ? begin + min(stop_all - begin, it.chunk) : stop_all;
   if (begin >= stop && it.split) return;
 
   const uint8_t* kc = c.k_codes + (int64_t)bh * c.capacity * D;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         o.w = fmaf(f, v.w, o.w);
       }
       if (it.split) {
-        float* part = it.part(a, r, it.chunk_id);
+        float* part = it.part(a, r, 0);
         *reinterpret_cast<float4*>(part + x) = o;
         if (x == 0) *reinterpret_cast<float2*>(part + D) = make_float2(M, L);
         continue;
@@ -469,11 +469,14 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) merge_q8_kernel(Q8Atten
   const int lane = threadIdx.x & 31, team = (threadIdx.x >> 5) / W, warp = (threadIdx.x >> 5) % W;
   const int64_t id = (int64_t)blockIdx.x * (kMergeWarps / W) + team;
   Q8Item it;
-  it.place(a, a.plan.whole + (int)min(id / a.plan.row_tile, (int64_t)(a.plan.units - a.plan.whole - 1)));
+  const int unit = a.plan.whole + (int)min(id / a.plan.row_tile, (int64_t)(a.plan.units - a.plan.whole - 1));
+  it.place_unit(a, unit);
+  it.first_item(a, unit);
   const int r = (int)(id % a.plan.row_tile), i = it.token(r);
   const Q8Seq seq(a, it.b);
   const bool live = id < (int64_t)(a.plan.units - a.plan.whole) * a.plan.row_tile && it.row0 + r < it.rows && i < seq.q_len;
-  const int nc = live ? (seq.limit(i) + a.plan.chunk - 1) / a.plan.chunk * a.plan.parts : 0, stride = a.plan.part_stride;
+  const int nc = live ? (seq.limit(i) + it.chunk - 1) / it.chunk * a.plan.parts : 0;
+  const int64_t step = Q8Item::part_step(a);
   const float* part = it.part(a, r, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float M = -INFINITY, L = 0.0f;  // of this warp's chunks
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) merge_q8_kernel(Q8Atten
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * W;
-      const float* pk = part + (int64_t)k * stride;
+      const float* pk = part + k * step;
       ml[u] = k < nc ? *reinterpret_cast<const float2*>(pk + D) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int p = 0; p < P; ++p)
@@ -597,7 +600,7 @@ cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream) {
 
 template <int D>
 static cudaError_t merge_rows(const Q8AttendArgs& a, cudaStream_t stream) {
-  const int W = a.plan.n_parts <= 8 ? 1 : a.plan.n_parts <= 64 ? 8 : 32, per_cta = W == 1 ? 8 : 1;
+  const int W = a.plan.row_parts <= 8 ? 1 : a.plan.row_parts <= 64 ? 8 : 32, per_cta = W == 1 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.plan.split_rows() + per_cta - 1) / per_cta));
   cfg.blockDim = dim3(W == 1 ? 256 : 32 * W);

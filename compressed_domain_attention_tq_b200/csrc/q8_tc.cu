@@ -540,8 +540,7 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
   const bool split = it.split;
   if (*abort) l = __int_as_float(0x7fc00000);
   const float f = none ? 0.0f : split ? ref : ref / l;
-  const int part_id = MODE == kQ8TwoStreams ? 2 * it.chunk_id + u : it.chunk_id;
-  float* part = it.part(a, local, part_id);
+  float* part = it.part(a, local, MODE == kQ8TwoStreams ? u : 0);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
     uint32_t o[32];
@@ -590,16 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Item it(a, blockIdx.x);
   const Q8Seq seq(a, it.b);
-  if (it.chunk_id == 0 && it.tile == 0 && it.hk == 0 && threadIdx.x == 0)
-    static_cast<int32_t*>(a.workspace)[it.b] = seq.bad;
+  q8_write_flags(a);
   const int first_i = it.row0 / it.G;
   const int q_last = min(min(it.rows - 1, it.row0 + a.plan.row_tile - 1) / it.G, seq.q_len - 1);
   const int stop_all = q_last < first_i ? 0 : seq.limit(q_last);
-  it.begin = it.chunk_id * a.plan.chunk;
-  it.stop = it.split ? min(stop_all, it.begin + a.plan.chunk) : stop_all;
+  it.begin = it.chunk_id * it.chunk;
+  it.stop = it.split ? it.begin + min(stop_all - it.begin, it.chunk) : stop_all;
   it.nt = max(0, (it.stop - it.begin + L::T - 1) / L::T);
   // nothing to do (rows that see no token get zeros here, or from the merge)
-  if (q_last < first_i || (it.nt == 0 && it.split)) return;
+  if (!it.any || q_last < first_i || (it.nt == 0 && it.split)) return;
 
   if (threadIdx.x == 0) {
 #pragma unroll
