@@ -361,6 +361,58 @@ def test_bf16_outputs_of_fp32_queries():
         check(c.attend(x.cuda(), i32([500, 90]), 500, attn_scale=0.1, out=out, workspace=ws), want, ref, [500, 90], None)
 
 
+@pytest.mark.parametrize("B", [2, 5, 32, 40])
+@pytest.mark.parametrize("n,G,dtype", [(1, 4, F32), (3, 8, BF16), (40, 8, BF16)])
+def test_ragged_batches_of_any_size(B, n, G, dtype):
+    """Batches split by their lengths (up to 32 sequences) and by the longest one (more)."""
+    rng = np.random.RandomState(B)
+    ctx = [int(x) for x in rng.randint(0, 1500, B)]
+    ctx[B // 2], ctx[-1] = 1500, 0
+    q_lens = None if n == 1 else [int(x) for x in rng.randint(0, n + 1, B)]
+    ref, c = build(64, 32, 1, ctx, "int8", seed=70, capacity=1500)
+    q = randn((B, G, n, 64), 71, dtype)
+    want, _ = ref.attend(f64(q), ctx, q_lens, 0.125)
+    got = c.attend(q.cuda(), i32(ctx), 1500, q_lens=None if q_lens is None else i32(q_lens))
+    check(got, want, ref, ctx, q_lens)
+    none = c.attend(q.cuda(), i32([0] * B), 1500)
+    assert torch.all(none == 0)
+
+
+@pytest.mark.parametrize("d,G", [(64, 24), (128, 64), (256, 17), (96, 32)])
+def test_decode_of_many_heads_in_bf16(d, G):
+    ctx = [700, 1, 257]
+    ref, c = build(d, 64, 1, ctx, "e4m3", seed=72)
+    q = randn((3, G, d), 73, BF16)
+    out = torch.empty(3, G, d, device="cuda", dtype=BF16)
+    want, _ = ref.attend(f64(q[:, :, None]), ctx, None, d ** -0.5)
+    check(c.decode(q.cuda(), i32(ctx), 700, out=out)[:, :, None], want, ref, ctx, None)
+    check(c.decode(q.cuda(), i32(ctx), 700)[:, :, None], want, ref, ctx, None)
+
+
+def test_a_captured_call_follows_the_lengths():
+    """Lengths are read on the device: a replay with others is the call with them."""
+    ref, c = build(128, 64, 2, [1800, 1800, 1800], "int8")
+    q1, qn = randn((3, 16, 128), 74, BF16).cuda(), randn((3, 16, 6, 128), 75, BF16).cuda()
+    ctx, lens = i32([1800, 1800, 1800]), i32([6, 6, 6])
+    one, many = torch.empty(3, 16, 128, device="cuda"), torch.empty_like(qn)
+    call = lambda: (c.decode(q1, ctx, 1800, out=one), c.attend(qn, ctx, 1800, q_lens=lens, out=many))  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for new, m in (([5, 1800, 64], [5, 6, 1]), ([0, 3, 1799], [0, 3, 6]), ([700, 640, 1000], [6, 6, 6])):
+        ctx.copy_(i32(new))
+        lens.copy_(i32(m))
+        many.fill_(7.0)
+        g.replay()
+        want_one, want_many = c.decode(q1, i32(new), 1800), c.attend(qn, i32(new), 1800, q_lens=i32(m))
+        torch.cuda.synchronize()
+        assert torch.equal(one, want_one)
+        for b in range(3):
+            assert torch.equal(many[b, :, :m[b]], want_many[b, :, :m[b]]) and torch.all(many[b, :, m[b]:] == 7.0)
+
+
 def test_a_pipeline_that_starves_ends_with_nan():
     """The first tile never arrives: the bounded waits run out and the outputs are NaN."""
     for n, d in ((64, 128), (8, 128), (64, 256)):
@@ -473,6 +525,16 @@ def test_rows_past_four_gigabytes():
         p = np.exp(kk @ f64(q)[0, h, 0])
         want = p @ vv / (p.sum() + pos)
         assert np.linalg.norm(out[0, h, 0] - want) <= REL_L2_GATE * np.linalg.norm(want)
+    # two tokens of nine heads each in bf16: rows 0 .. pos + 98 and .. pos + 99
+    q = randn((1, 18, 2, d), 53, BF16)
+    out = f64(c.attend((q * 2).cuda(), i32([pos + 100]), cap, attn_scale=0.5))
+    for h in range(18):
+        kk, vv = ref.values(0, 0, h // 9, at, at + 100), ref.values(1, 0, h // 9, at, at + 100)
+        for i in range(2):
+            m = 99 + i
+            p = np.exp(kk[:m] @ f64(q)[0, h, i])
+            want = p @ vv[:m] / (p.sum() + pos)
+            assert np.all(np.abs(out[0, h, i] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(vv).max())
 
 
 def test_python_calls_refuse():
