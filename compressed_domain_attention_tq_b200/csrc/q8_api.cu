@@ -91,7 +91,7 @@ bool make_q8_plan(int B, int Hq, int Hkv, int d, int n, int max_ctx, bool bf16, 
     p->row_tile = p->mode == kQ8TwoRows ? 256 : 128;
     p->parts = p->mode == kQ8TwoStreams ? 2 : 1;
     per_sm = 1;
-    step = p->parts * q8_tc_tile_tokens(d);
+    step = p->parts * q8_tc_tile_tokens(d, p->mode);
     item_cost = 512;
   } else {
     p->mode = kQ8Warps;

@@ -83,7 +83,7 @@ cudaError_t launch_q8_append(const Q8WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t stream);
 int q8_split_per_sm(int d, int row_tile);  // work items of the split kernel resident on an SM
 cudaError_t launch_q8_split(const Q8AttendArgs& a, cudaStream_t stream);
-int q8_tc_tile_tokens(int d);             // tokens of one step of the tensor-memory kernel
+int q8_tc_tile_tokens(int d, Q8Mode mode);  // tokens of one step of the tensor-memory kernel
 cudaError_t launch_q8_tc(const Q8AttendArgs& a, cudaStream_t stream);
 cudaError_t launch_q8_merge(const Q8AttendArgs& a, cudaStream_t stream);
 

@@ -6,10 +6,10 @@
 // Rows.  As in q8_split.cu the query rows of a kv head are its n tokens x G query
 // heads, row r = i G + g, cut into tiles of 128 (the M of one product).  With
 // S = Q K^T (128 rows x T tokens) and O (128 x d) += P V a CTA holds, by mode:
-//   two row tiles (d <= 128, more than 128 rows): both use each tile of T = 128
-//     tokens, so a code is converted once for 256 rows;
+//   two row tiles (d <= 128, more than 128 rows): both use each token tile, so a code is
+//     converted once for 256 rows (T = 128; 64 and two S for each row tile at d = 64);
 //   two token streams (d <= 128, up to 128 rows): one row tile, the even token
-//     tiles in one (S, O), the odd ones in the other; each writes its own partial;
+//     tiles (T = 128) in one (S, O), the odd ones in the other; each writes its own partial;
 //   one stream (d = 256, T = 64): one row tile, two S, one O.
 // In each the products of one S run while the softmax of the other does.
 //
@@ -63,40 +63,51 @@ constexpr float kShift = 7.0f, kTopSum = 32768.0f;
 constexpr float kMasked = -3e38f, kMinRatio = 0x1p-40f;
 constexpr int kScaleSlots = 4, kPrefetch = 2;
 
-// tokens of a tile; what a column of its operands (8 dims of all tokens) is longer than them
-__host__ __device__ constexpr int tile_tokens(int d) { return d <= 128 ? 128 : 64; }
+// Tokens of a tile.  With 64 there is room for a second score tile of each row tile, so that
+// the softmax does not wait for its products, but products of 64 columns read Q from shared
+// memory twice as often: 434 us against 459 for a 2048-token chunk at 8K with d = 64, 1117
+// against 946 at 16K with d = 128, 319 against 309 with d = 96.
+__host__ __device__ constexpr int tile_tokens(int d, int mode) {
+  return d > 128 || (d == 64 && mode == kQ8TwoRows) ? 64 : 128;
+}
+// what a column of its operands (8 dims of all tokens) is longer than them
 __host__ __device__ constexpr int column_pad(int d) { return d == 96 ? 32 : 16; }
 
 template <int D, int MODE>
 struct Layout {
-  static constexpr int T = tile_tokens(D);
+  static constexpr int T = tile_tokens(D, MODE), H = 64, NH = T / H;  // halves of a tile of 128
   static constexpr int QT = MODE == kQ8TwoRows ? 2 : 1;
+  static constexpr int NS = D <= 128 && T == 64 ? 4 : 2;   // tiles of K and of V in shared memory
+  static constexpr int kUnits = MODE == kQ8TwoRows ? 2 : 1;
+  static constexpr int NB = kUnits == 2 && T == 64 ? 4 : 2;  // score tiles in tensor memory
+  static constexpr int kAhead = NB / kUnits;                 // of one row tile
   // Row r of a tile sits at place r ^ kRowFlip: up to 64 rows then belong to the warps of the
-  // two schedulers that have one converter each, not two (5 drafts at 128K: FLIP_TIMES).
+  // two schedulers that have one converter each, not two (5 drafts x 8 sequences:
+  // 134 -> 131 us).
   static constexpr int kRowFlip = MODE == kQ8TwoRows ? 0 : 64;
   static constexpr int Q_BYTES = 128 * D * 2, COLUMN = T * 16 + column_pad(D), KV_BYTES = D / 8 * COLUMN;
-  static constexpr int Q = 0, K = Q + QT * Q_BYTES, V = K + 2 * KV_BYTES;
-  static constexpr int CROW = V + 2 * KV_BYTES;             // float [QT * 128]
+  static constexpr int Q = 0, K = Q + QT * Q_BYTES, V = K + NS * KV_BYTES;
+  static constexpr int CROW = V + NS * KV_BYTES;            // float [QT * 128]
   static constexpr int SCALES = CROW + 4 * QT * 128;        // float4 [kScaleSlots][T / 16]
   static constexpr int BAR = SCALES + 16 * kScaleSlots * (T / 16);
-  static constexpr int MISC = BAR + 8 * 32;                 // tmem base, abort, ref, warp maxima
+  static constexpr int MISC = BAR + 8 * 40;                 // tmem base, abort, ref, warp maxima
   static constexpr int BYTES = MISC + 16 + 4 * kWarps;
   static_assert(BYTES <= 227 * 1024, "shared memory");
   static __host__ __device__ constexpr uint32_t S(int b) { return (uint32_t)(b * T); }
-  static __host__ __device__ constexpr uint32_t O(int u) { return (uint32_t)(2 * T + u * D); }
+  static __host__ __device__ constexpr uint32_t O(int u) { return (uint32_t)(NB * T + u * D); }
 };
 
 enum Bar : int {
-  kKFull = 0,    // [2] K operand written (convert warps)
-  kKEmpty = 2,   // [2] its products done (commit)
-  kVFull = 4,
-  kVEmpty = 6,
-  kSFull = 8,    // [2] scores in tensor memory (commit)
-  kPFull = 10,   // [2][2] the halves of the weights in tensor memory (4 softmax warps)
-  kPVDone = 14,  // [2][2] O up to date with that half of a tile (commit)
-  kScFull = 18,  // [kScaleSlots] block scales written (one warp)
-  kDone = 22,    // every product complete (commit)
-  kBars = 23
+  kKFull = 0,    // [NS] K operand written (convert warps)
+  kKEmpty = 4,   // [NS] its products done (commit)
+  kVFull = 8,
+  kVEmpty = 12,
+  kSFull = 16,   // [NB] scores in tensor memory (commit)
+  kPFull = 20,   // [NB][NH] weights of a half in tensor memory (4 softmax warps)
+  kPVDone = 24,  // [units][NH] O up to date with that half of a tile (commit)
+  kScFull = 28,  // [kScaleSlots] block scales written (one warp)
+  kDone = 32,    // every product complete (commit)
+  kBars = 33
 };
 
 // What one CTA does: a work item's rows, and tokens [begin, stop) in nt tiles.
@@ -151,9 +162,9 @@ __device__ __forceinline__ void rescale(uint32_t col, float alpha) {
 // neighbouring lanes take kC pieces of each of kT tokens: a load touches few lines (with
 // eight tokens a load it took 28 clocks of the SM, not 8), and with the columns of the
 // operand kPad bytes further apart their stores fill all banks.
-template <int D>
+template <int D, int T>
 struct Pieces {
-  static constexpr int T = tile_tokens(D), C = D / 16, N = (T * C + kConvertThreads - 1) / kConvertThreads;
+  static constexpr int C = D / 16, N = (T * C + kConvertThreads - 1) / kConvertThreads;
   static constexpr int kC = D == 96 ? 2 : 4, kT = 8 / kC, kPad = column_pad(D);
   static constexpr int kStep = kConvertThreads / C;  // tokens from one piece of a thread to the next
   static_assert(kConvertThreads % (8 * C / kC) == 0, "a thread's pieces are the same bytes of their tokens");
@@ -212,12 +223,12 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
   uint64_t* full = bar + (is_v ? kVFull : kKFull);
   uint64_t* empty = bar + (is_v ? kVEmpty : kKEmpty);
   unsigned char* operand = smem + (is_v ? L::V : L::K);
-  Pieces<D> x;
+  Pieces<D, L::T> x;
   if (it.nt > 0) x.load(tile, it.stop - it.begin, tid);
 #pragma unroll 1
   for (int j = 0; j < it.nt; ++j) {
-    const int s = j & 1;
-    if (j >= 2) warp_wait(empty + s, ((j >> 1) - 1) & 1, abort);
+    const int s = j % L::NS;
+    if (j >= L::NS) warp_wait(empty + s, (j / L::NS - 1) & 1, abort);
     tile += L::T * D;
     const int rows = it.stop - it.begin - (j + 1) * L::T;  // of the next tile
     if (rows >= L::T)
@@ -267,7 +278,7 @@ __device__ __forceinline__ void scale_role(const Q8AttendArgs& a, const Item& it
     // slot j - 4 has been read once the scores of tile j - 2 are done: they came after the
     // weights of tile j - 4
     const int slot = j & (kScaleSlots - 1);
-    if (j >= 2) warp_wait(bar + kKEmpty + (j & 1), ((j >> 1) - 1) & 1, abort);
+    if (j >= 2) warp_wait(bar + kKEmpty + (j - 2) % L::NS, ((j - 2) / L::NS) & 1, abort);
     if (lane < L::T / 16) reinterpret_cast<float4*>(smem + L::SCALES)[slot * (L::T / 16) + lane] = k;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + kScFull + slot);
@@ -292,7 +303,7 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
   };
   // scores of token tile j into S[b], from row tile u of Q
   auto scores = [&](int j, int u, int b) {
-    const uint32_t q = at + ((L::Q + u * L::Q_BYTES) >> 4), k = at + ((L::K + (j & 1) * L::KV_BYTES) >> 4);
+    const uint32_t q = at + ((L::Q + u * L::Q_BYTES) >> 4), k = at + ((L::K + j % L::NS * L::KV_BYTES) >> 4);
     if (leader && !*abort) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
@@ -300,66 +311,51 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
     }
     commit(kSFull + b);
   };
-  // O[u] += P[b] V of half h of token tile j, once its weights are there
-  auto values = [&](int j, int h, int u, int b, uint32_t phase, bool first) {
-    const uint32_t v = at + ((L::V + (j & 1) * L::KV_BYTES) >> 4);
-    constexpr int H = L::T / 32;  // products of 16 tokens in a half
-    warp_wait(bar + kPFull + 2 * b + h, phase, abort);
-    fence_after();
-    if (leader && !*abort) {
+  // O[u] += P[b] V of token tile j, half by half as their weights come
+  auto values = [&](int j, int u, int b, bool first) {
+    const uint32_t v = at + ((L::V + j % L::NS * L::KV_BYTES) >> 4);
+    constexpr int n = L::H / 16;  // products of 16 tokens in a half
 #pragma unroll
-      for (int c = 0; c < H; ++c)
-        mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * (h * H + c), v0 | (v + (h * H + c) * 16), idO, c > 0 || !first);
+    for (int h = 0; h < L::NH; ++h) {
+      warp_wait(bar + kPFull + b * L::NH + h, (j / L::kAhead) & 1, abort);
+      fence_after();
+      if (leader && !*abort) {
+#pragma unroll
+        for (int c = h * n; c < (h + 1) * n; ++c)
+          mma_ts(tbase + L::O(u), tbase + L::S(b) + 8 * c, v0 | (v + c * 16), idO, c > 0 || !first);
+      }
+      commit(kPVDone + u * L::NH + h);
     }
-    commit(kPVDone + 2 * u + h);
   };
   auto wait_k = [&](int j) {
-    warp_wait(bar + kKFull + (j & 1), (j >> 1) & 1, abort);
+    warp_wait(bar + kKFull + j % L::NS, (j / L::NS) & 1, abort);
     fence_after();
   };
   auto wait_v = [&](int j) {
-    warp_wait(bar + kVFull + (j & 1), (j >> 1) & 1, abort);
+    warp_wait(bar + kVFull + j % L::NS, (j / L::NS) & 1, abort);
     fence_after();
   };
-  if constexpr (MODE == kQ8TwoRows) {
-    wait_k(0);
-    scores(0, 0, 0);
-    scores(0, 1, 1);
-    commit(kKEmpty);
-#pragma unroll 1
-    for (int j = 0; j < it.nt; ++j) {
-      wait_v(j);
+  for (int j = 0; j < L::kAhead && j < it.nt; ++j) {
+    wait_k(j);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        values(j, 0, u, u, j & 1, j == 0);
-        values(j, 1, u, u, j & 1, false);
-        if (j + 1 < it.nt) {
-          if (u == 0) wait_k(j + 1);
-          scores(j + 1, u, u);
-        }
-      }
-      commit(kVEmpty + (j & 1));
-      if (j + 1 < it.nt) commit(kKEmpty + ((j + 1) & 1));
-    }
-  } else {
-    for (int j = 0; j < 2 && j < it.nt; ++j) {
-      wait_k(j);
-      scores(j, 0, j);
-      commit(kKEmpty + j);
-    }
+    for (int u = 0; u < L::kUnits; ++u) scores(j, u, L::kAhead * u + j);
+    commit(kKEmpty + j);
+  }
 #pragma unroll 1
-    for (int j = 0; j < it.nt; ++j) {
-      const int b = j & 1, u = MODE == kQ8TwoStreams ? b : 0;
-      wait_v(j);
-      values(j, 0, u, b, (j >> 1) & 1, MODE == kQ8TwoStreams ? j < 2 : j == 0);
-      values(j, 1, u, b, (j >> 1) & 1, false);
-      commit(kVEmpty + b);
-      if (j + 2 < it.nt) {
-        wait_k(j + 2);
-        scores(j + 2, 0, b);
-        commit(kKEmpty + b);
+  for (int j = 0; j < it.nt; ++j) {
+    const int next = j + L::kAhead;
+    wait_v(j);
+#pragma unroll
+    for (int u = 0; u < L::kUnits; ++u) {
+      const int b = L::kAhead * u + j % L::kAhead;
+      values(j, MODE == kQ8TwoStreams ? b : u, b, MODE == kQ8TwoStreams ? j < 2 : j == 0);
+      if (next < it.nt) {
+        if (u == 0) wait_k(next);
+        scores(next, u, b);
       }
     }
+    commit(kVEmpty + j % L::NS);
+    if (next < it.nt) commit(kKEmpty + next % L::NS);
   }
   commit(kDone);
   if (leader) mbar_drain(bar + kDone, 0);
@@ -480,22 +476,21 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
   const int ou = MODE == kQ8OneStream ? 0 : u;
   int n = 0;  // tiles done
   for (int j = MODE == kQ8TwoStreams ? u : 0; j < nt; j += step, ++n) {
-    const int sb = MODE == kQ8TwoRows ? u : (j & 1);
-    const int phase = MODE == kQ8TwoRows ? j : (j >> 1);
+    const int sb = (MODE == kQ8TwoRows ? L::kAhead * u : 0) + j % L::kAhead;
     const uint32_t s_col = tbase + lanes + L::S(sb);
     warp_wait(bar + kScFull + (j & (kScaleSlots - 1)), (j / kScaleSlots) & 1, abort);
     const float4* sc = reinterpret_cast<const float4*>(smem + L::SCALES) + (j & (kScaleSlots - 1)) * (T / 16);
-    warp_wait(bar + kSFull + sb, phase & 1, abort);
+    warp_wait(bar + kSFull + sb, (j / L::kAhead) & 1, abort);
     fence_after();
-    // Each half is a step of the online softmax of its own: its product starts while the
-    // other half's weights are computed, and 64 scores fit in registers.  The weights are
+    // 64 tokens are a step of the online softmax: that many scores fit in registers, and the
+    // product of one half of a tile of 128 starts while the other's weights are computed.  The weights are
     // computed with the reference as it is; if 16 of them sum to more than kTopSum
     // (f16 would overflow soon) it is moved and they are computed again, so that no maximum
     // has to be taken otherwise.
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < L::NH; ++h) {
       if (warp_live) {
-        constexpr int H = T / 2;
+        constexpr int H = L::H;
         Half<H> x;
         const float4* sch = sc + h * (H / 16);
         const int tok0 = begin + j * T + h * H;
@@ -511,8 +506,9 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
           m = mn;
           l *= alpha;
           if (n + h > 0) {  // once O is up to date
-            if (n > 0) warp_wait(bar + kPVDone + 2 * ou + 1, (n - 1) & 1, abort);
-            if (h > 0) warp_wait(bar + kPVDone + 2 * ou, n & 1, abort);
+            // (the scores at hand came after all but the last tile's product)
+            if (n > 0) warp_wait(bar + kPVDone + (ou + 1) * L::NH - 1, (n - 1) & 1, abort);
+            if (h > 0) warp_wait(bar + kPVDone + ou * L::NH, n & 1, abort);
             fence_after();
             rescale<D>(tbase + lanes + L::O(ou), alpha);
           }
@@ -524,7 +520,7 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
         fence_before();
         __syncwarp();
       }
-      if (lane == 0) mbar_arrive(bar + kPFull + 2 * sb + h);
+      if (lane == 0) mbar_arrive(bar + kPFull + sb * L::NH + h);
     }
   }
   if (nt > 0) warp_wait(bar + kDone, 0, abort);
@@ -601,15 +597,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
 
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar + kKFull + i, kConvertWarps);
       mbar_init(bar + kKEmpty + i, 1);
       mbar_init(bar + kVFull + i, kConvertWarps);
       mbar_init(bar + kVEmpty + i, 1);
       mbar_init(bar + kSFull + i, 1);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
       mbar_init(bar + kPFull + i, 4);
       mbar_init(bar + kPVDone + i, 1);
     }
@@ -743,7 +736,7 @@ cudaError_t launch_format(const Q8AttendArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int q8_tc_tile_tokens(int d) { return tile_tokens(d); }
+int q8_tc_tile_tokens(int d, Q8Mode mode) { return tile_tokens(d, mode); }
 
 cudaError_t launch_q8_tc(const Q8AttendArgs& a, cudaStream_t stream) {
   return a.c.e4m3 ? launch_format<E4m3>(a, stream) : launch_format<Int8>(a, stream);
