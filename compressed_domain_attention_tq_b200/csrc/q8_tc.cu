@@ -240,8 +240,17 @@ __device__ __forceinline__ void convert_role(const Q8AttendArgs& a, const Item& 
   }
 }
 
-// Codes are brought into L2 kPrefetch tiles before the converters load them: their registers
-// hold one tile of K and one of V, 32 KB an SM, which at HBM's latency is 3 TB/s.
+// Codes of tile j into L2, kPrefetch tiles before the converters load them (the first ones
+// while the queries are prepared): their registers hold one tile of K and one of V.
+template <int D, int MODE>
+__device__ __forceinline__ void prefetch_tile(const Q8AttendArgs& a, const Item& it, int j) {
+  constexpr int T = Layout<D, MODE>::T;
+  if (j >= it.nt) return;
+  const int tok0 = it.begin + j * T, bytes = min(T, it.stop - tok0) * D;
+  prefetch_l2(head_codes<D>(a.c.k_codes, a, it.bh) + (int64_t)tok0 * D, bytes);
+  prefetch_l2(head_codes<D>(a.c.v_codes, a, it.bh) + (int64_t)tok0 * D, bytes);
+}
+
 // For each 16 tokens of a tile {s_k, log2(s_v / ref), ref / s_v}: a warp of its own, since
 // the logarithm and the divisions held a converter up for a third of its time.
 template <int D, int MODE>
@@ -258,20 +267,10 @@ __device__ __forceinline__ void scale_role(const Q8AttendArgs& a, const Item& it
     sk = __ldg(ksc + blk);
     sv = __ldg(vsc + blk);
   };
-  // codes of tile j into L2
-  const uint8_t* kc = head_codes<D>(a.c.k_codes, a, it.bh);
-  const uint8_t* vc = head_codes<D>(a.c.v_codes, a, it.bh);
-  auto prefetch = [&](int j) {
-    if (j >= it.nt || lane != 0) return;
-    const int tok0 = it.begin + j * L::T, bytes = min(L::T, it.stop - tok0) * D;
-    prefetch_l2(kc + (int64_t)tok0 * D, bytes);
-    prefetch_l2(vc + (int64_t)tok0 * D, bytes);
-  };
-  for (int j = 1; j < kPrefetch; ++j) prefetch(j);
   load(0);
 #pragma unroll 1
   for (int j = 0; j < it.nt; ++j) {
-    prefetch(j + kPrefetch);
+    if (lane == 0) prefetch_tile<D, MODE>(a, it, j + kPrefetch);
     const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
     const float4 k = make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
     load(j + 1);
@@ -595,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
   // nothing to do (rows that see no token get zeros here, or from the merge)
   if (!it.any || q_last < first_i || (it.nt == 0 && it.split)) return;
 
+  if (warp == kScaleWarp && lane == 0)
+    for (int j = 0; j < kPrefetch; ++j) prefetch_tile<D, MODE>(a, it, j);
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
