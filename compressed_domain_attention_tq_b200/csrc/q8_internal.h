@@ -46,6 +46,7 @@ enum Q8Mode : int { kQ8Warps, kQ8TwoRows, kQ8TwoStreams, kQ8OneStream };
 // `target` items share the tokens of a ragged batch evenly.
 struct Q8Plan {
   int row_tile;     // rows of one work item
+  int merge_rows;   // of them that any unit has
   int tiles;        // ceil(n * G / row_tile)
   int whole, units;
   int chunk, n_chunks;
@@ -59,7 +60,7 @@ struct Q8Plan {
   int64_t split_items() const { return target ? target : (int64_t)(units - whole) * n_chunks; }
   int64_t items() const { return whole + split_items(); }
   int row_parts;    // partial results of a row, about
-  int64_t split_rows() const { return (int64_t)(units - whole) * row_tile; }
+  int64_t split_rows() const { return (int64_t)(units - whole) * merge_rows; }
 };
 
 struct Q8AttendArgs {

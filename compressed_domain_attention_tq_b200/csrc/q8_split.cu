@@ -469,12 +469,12 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) merge_q8_kernel(Q8Atten
   const int lane = threadIdx.x & 31, team = (threadIdx.x >> 5) / W, warp = (threadIdx.x >> 5) % W;
   const int64_t id = (int64_t)blockIdx.x * (kMergeWarps / W) + team;
   Q8Item it;
-  const int unit = a.plan.whole + (int)min(id / a.plan.row_tile, (int64_t)(a.plan.units - a.plan.whole - 1));
+  const int unit = a.plan.whole + (int)min(id / a.plan.merge_rows, (int64_t)(a.plan.units - a.plan.whole - 1));
   it.place_unit(a, unit);
   it.first_item(a, unit);
-  const int r = (int)(id % a.plan.row_tile), i = it.token(r);
+  const int r = (int)(id % a.plan.merge_rows), i = it.token(r);
   const Q8Seq seq(a, it.b);
-  const bool live = id < (int64_t)(a.plan.units - a.plan.whole) * a.plan.row_tile && it.row0 + r < it.rows && i < seq.q_len;
+  const bool live = id < (int64_t)(a.plan.units - a.plan.whole) * a.plan.merge_rows && it.row0 + r < it.rows && i < seq.q_len;
   const int nc = live ? (seq.limit(i) + it.chunk - 1) / it.chunk * a.plan.parts : 0;
   const int64_t step = Q8Item::part_step(a);
   const float* part = it.part(a, r, 0);
