@@ -380,8 +380,16 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         const uint32_t f[4] = {f01[2 * h], f01[2 * h + 1], f23[2 * h], f23[2 * h + 1]};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma(acc[nt][2 * w + h], f, whi[nt][0], whi[nt][1]);
-          mma(acc[nt][2 * w + h], f, wlo[nt][0], wlo[nt][1]);
+          // a step's sum of its own, added with rounding to nearest: the tensor cores cut
+          // off below the accumulator's last bit, which over hundreds of steps (d = 256 at
+          // 64K) was the largest error of all
+          float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma(o, f, wlo[nt][0], wlo[nt][1]);
+          mma(o, f, whi[nt][0], whi[nt][1]);
+          float(&sum)[4] = acc[nt][2 * w + h];
+          const float2 s0 = add2(make_float2(sum[0], sum[1]), make_float2(o[0], o[1]));
+          const float2 s1 = add2(make_float2(sum[2], sum[3]), make_float2(o[2], o[3]));
+          sum[0] = s0.x, sum[1] = s0.y, sum[2] = s1.x, sum[3] = s1.y;
         }
       }
     }
