@@ -23,15 +23,17 @@
 // 2^(x - m) s_v / ref with x = S s_k scale log2(e), m the row's reference (moved
 // only when weights get large) and ref the item's largest V scale; it is
 // rounded to f16's 11 bits, as the bf16 output keeps 8.  The ratio enters as
-// its logarithm in the exponent, so it costs nothing; it is floored at 2^-40:
-// a block whose scale is that far below ref then counts with at most
-// 2^-40 max|v|, far below the output's rounding.  Row sums and O are fp32.
+// its logarithm in the exponent, so it costs nothing, and m is taken from scores with it,
+// so weights of a row that sees only small blocks are as exact as others.  It is floored
+// at 2^-90 (sums of 2^(x - m) stay in fp32's range): a block whose scale is further below
+// ref counts as if it were there, with at most 2^-90 of the item's largest value.  Row
+// sums and O are fp32.
 //
 // Operand layout in shared memory, without swizzle: [d / 8][rows][16 bytes] (and a pad
-// after each column of rows), an 8 x 16-byte core matrix contiguous.  For K that is K-major (rows = tokens), and
-// the same bytes are MN-major for V, so one converter serves both.  int8 codes leave the
-// converter in the order 0 2 1 3 of each word: Q is stored in that order, and
-// O's columns are put back when they are written.
+// after each column of rows), an 8 x 16-byte core matrix contiguous.  For K that is K-major
+// (rows = tokens), and the same bytes are MN-major for V, so one converter serves both.  int8
+// codes leave the converter in the order 0 2 1 3 of each word: Q is stored in that order,
+// and O's columns are put back when they are written.
 //
 // Bound: for long chunks the exponentials and the products in turn (the softmax of one
 // row tile overlaps the other's products, 41% to 49% of the tensor cores' time each):
@@ -63,10 +65,12 @@ constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 // kCubic of every 8 pairs of exponentials take the cubic on the FMA pipe: 16 a clock and SM
 // would bound the tile (2 x 128 x 128 of them in the 2048 clocks of its products)
 constexpr int kCubic = 2;
-// as in q8_split.cu the reference is held 2^kShift below the maximum it was taken from, and
-// moves when weights reach 2^15
-constexpr float kShift = 7.0f, kTopSum = 32768.0f;
-constexpr float kMasked = -3e38f, kMinRatio = 0x1p-40f;
+// The reference is held 2^kShift below the maximum it was taken from, and moves when 16
+// weights sum to 2^15.  With 7 it moved more often (2048-token chunk at 16K with outliers
+// 1120 us against 1046); weights keep 11 bits down to 2^-18 of the largest, and 2^-28 of it
+// is their last bit.
+constexpr float kShift = 4.0f, kTopSum = 32768.0f;
+constexpr float kMasked = -3e38f, kMinRatio = 0x1p-90f;
 constexpr int kScaleSlots = 4, kPrefetch = 2;
 
 // Tokens of a tile.  With 64 there is room for a second score tile of each row tile, so that
@@ -411,7 +415,8 @@ struct Half {
       if (i >= left) s[i / 32][i % 32] = __float_as_uint(kMasked);
   }
 
-  // the largest score in log2 units
+  // The largest weight's logarithm before the reference is taken off: with the blocks' V
+  // scales, so that weights keep their bits where a row sees only blocks far below ref.
   __device__ __forceinline__ float max(const float4* sc, float crow) const {
     float mx = -INFINITY;
 #pragma unroll
@@ -419,7 +424,7 @@ struct Half {
       float top = at(16 * g);
 #pragma unroll
       for (int i = 16 * g + 1; i < 16 * g + 16; ++i) top = fmaxf(top, at(i));
-      mx = fmaxf(mx, top * factor(sc[g].x, crow));
+      mx = fmaxf(mx, fmaf(top, factor(sc[g].x, crow), sc[g].y));
     }
     return mx;
   }

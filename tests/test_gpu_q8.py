@@ -261,6 +261,26 @@ def test_attend_with_scales_far_apart(fmt, n):
         check(c.attend(qb.cuda(), i32(ctx), 400, attn_scale=scale), want, ref, ctx, None, f"bf16 {size}")
 
 
+@pytest.mark.parametrize("d,G,n", [(128, 2, 160), (128, 4, 20), (256, 2, 60)])
+def test_rows_before_a_huge_block_keep_their_precision(d, G, n):
+    """A prompt whose last block of V is 1e7 or 1e20 times the others: the queries before it are exact
+    to their own values (weights of 11 bits and the output's rounding, as in check)."""
+    ctx = [n + 100]
+    for size in (1e7, 1e20):
+        ref, c = pair(1, 1, ctx[0], d, 16, "int8")
+        k, v = randn((1, 1, ctx[0], d), 80), randn((1, 1, ctx[0], d), 81)
+        last = (ctx[0] - 1) // 16 * 16
+        v[:, :, last:] *= size
+        ref.append(f64(k), f64(v), [0])
+        ref.upload(c)
+        q = randn((1, G, n, d), 82, BF16)
+        want, _ = ref.attend(f64(q), ctx, None, d ** -0.5)
+        got = f64(c.attend(q.cuda(), i32(ctx), ctx[0]))
+        vmax = ref.absmax_v(0, 0, last)
+        m = last - 100  # queries at positions below the block
+        assert np.all(np.abs(got - want)[:, :, :m] <= 2.0 ** -8 * np.abs(want[:, :, :m]) + 2.0 ** -10 * vmax)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_a_sharp_softmax_picks_its_row(n):
     """Scores hundreds apart: the weights of all rows but one vanish, and the reference moves many times."""
