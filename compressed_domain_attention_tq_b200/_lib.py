@@ -159,6 +159,7 @@ TEST_HOOK_FAIL_LAUNCH = 1
 TEST_HOOK_STARVE_PIPELINE = 2
 TEST_HOOK_TCGEN05_DECODE = 4
 TEST_HOOK_BUTTERFLY_QUANTIZE = 8
+TEST_HOOK_SLOW_SCALES = 16
 
 
 def set_test_hooks(hooks: int) -> None:

@@ -166,6 +166,7 @@ tq_status attend(const void* q, tq_dtype q_dtype, int32_t num_q_heads, int32_t n
   const unsigned hooks = g_test_hooks.load(std::memory_order_relaxed);
   if (hooks & TQ_TEST_HOOK_FAIL_LAUNCH) return status_of(cudaErrorLaunchFailure, where);
   a.test_starve = (hooks & TQ_TEST_HOOK_STARVE_PIPELINE) != 0;
+  a.test_slow_scales = (hooks & TQ_TEST_HOOK_SLOW_SCALES) != 0;
   cudaError_t e = append ? launch_q8_append(*append, stream) : cudaSuccess;
   if (e == cudaSuccess) e = a.plan.mode == kQ8Warps ? launch_q8_split(a, stream) : launch_q8_tc(a, stream);
   if (e == cudaSuccess && a.plan.whole < a.plan.units) e = launch_q8_merge(a, stream);

@@ -75,7 +75,7 @@ struct Q8AttendArgs {
   float* lse;  // [B][Hq][n][2] or NULL
   void* workspace;
   Q8Plan plan;
-  int test_starve;
+  int test_starve, test_slow_scales;
 };
 
 bool q8_head_dim_supported(int d);

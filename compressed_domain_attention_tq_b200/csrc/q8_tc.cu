@@ -116,8 +116,9 @@ enum Bar : int {
   kPFull = 20,   // [NB][NH] weights of a half in tensor memory (4 softmax warps)
   kPVDone = 24,  // [units][NH] O up to date with that half of a tile (commit)
   kScFull = 28,  // [kScaleSlots] block scales written (one warp)
-  kDone = 32,    // every product complete (commit)
-  kBars = 33
+  kScEmpty = 32, // [kScaleSlots] read: every weight of the tile is there (product warp)
+  kDone = 36,    // every product complete (commit)
+  kBars = 37
 };
 
 // What one CTA does: a work item's rows, and tokens [begin, stop) in nt tiles.
@@ -284,10 +285,12 @@ __device__ __forceinline__ void scale_role(const Q8AttendArgs& a, const Item& it
     const float ratio = ref > 0.0f ? fmaxf(sv / ref, kMinRatio) : 1.0f;
     const float4 k = make_float4(sk, log2f(ratio), 1.0f / ratio, 0.0f);
     load(j + 1);
-    // slot j - 4 has been read once the scores of tile j - 2 are done: they came after the
-    // weights of tile j - 4
+    if (a.test_slow_scales) __nanosleep(20000);
+    // The slot was tile j - 4's.  Its barrier cannot pass two phases while this warp is late
+    // (the parity would then read as not yet): the next one takes tile j's own scales.  The
+    // operands' barriers would not do, as tile j's scores need no scales.
     const int slot = j & (kScaleSlots - 1);
-    if (j >= 2) warp_wait(bar + kKEmpty + (j - 2) % L::NS, ((j - 2) / L::NS) & 1, abort);
+    if (j >= kScaleSlots) warp_wait(bar + kScEmpty + slot, (j / kScaleSlots - 1) & 1, abort);
     if (lane < L::T / 16) reinterpret_cast<float4*>(smem + L::SCALES)[slot * (L::T / 16) + lane] = k;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar + kScFull + slot);
@@ -363,6 +366,7 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
         scores(next, u, b);
       }
     }
+    if (leader) mbar_arrive(bar + kScEmpty + (j & (kScaleSlots - 1)));
     commit(kVEmpty + j % L::NS);
     if (next < it.nt) commit(kKEmpty + next % L::NS);
   }
@@ -619,7 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
       mbar_init(bar + kPVDone + i, 1);
     }
 #pragma unroll
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar + kScFull + i, 1);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(bar + kScFull + i, 1);
+      mbar_init(bar + kScEmpty + i, 1);
+    }
     mbar_init(bar + kDone, 1);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

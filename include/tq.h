@@ -663,12 +663,16 @@ TQ_API tq_status tq_sdpa_q8_decode_append(
  *  - TQ_TEST_HOOK_BUTTERFLY_QUANTIZE: bulk quantize-appends of bf16 vectors
  *    at head_dim 128 with rotation rotate with fp32 butterflies on the CUDA
  *    cores instead of the tensor-core product (for comparing the two).
+ *  - TQ_TEST_HOOK_SLOW_SCALES: in the tcgen05 attention over a q8 cache the
+ *    blocks' scales come 20 us late for each tile of tokens (as from a
+ *    congested memory); the results are the same.
  * No counterpart on the method's pages.
  */
 #define TQ_TEST_HOOK_FAIL_LAUNCH 1u
 #define TQ_TEST_HOOK_STARVE_PIPELINE 2u
 #define TQ_TEST_HOOK_TCGEN05_DECODE 4u
 #define TQ_TEST_HOOK_BUTTERFLY_QUANTIZE 8u
+#define TQ_TEST_HOOK_SLOW_SCALES 16u
 TQ_API void tq_set_test_hooks(uint32_t hooks);
 
 /* tq_status_string -- static English text for a status code. */
