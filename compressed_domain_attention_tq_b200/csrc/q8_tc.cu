@@ -37,9 +37,9 @@
 //
 // Bound: for long chunks the exponentials and the products in turn (the softmax of one
 // row tile overlaps the other's products, 41% to 49% of the tensor cores' time each):
-// 2048 tokens of 64/8 heads at 16K, d 128, 945 us = 1.09 PFLOP/s, 66% of the measured
-// matrix-product rate; d 256 (32/16 heads, 1024 tokens at 8K) 261 us = 0.99; d 96 262 us
-// = 0.69 and d 64 430 us = 0.56, whose products are shorter per exponential.  For few rows
+// 2048 tokens of 64/8 heads at 16K, d 128, 960 us = 1.07 PFLOP/s, 65% of the measured
+// matrix-product rate; d 256 (32/16 heads, 1024 tokens at 8K) 258 us = 1.00; d 96 260 us
+// = 0.69 and d 64 425 us = 0.57, whose products are shorter per exponential.  For few rows
 // the chain of products and softmax of a token tile, 2100 clocks where HBM would need
 // 1420: 5 drafted tokens at 128K 84 us, 3.2 TB/s.
 #include <limits.h>
@@ -376,18 +376,28 @@ __device__ __forceinline__ void mma_role(const Item& it, unsigned char* smem, ui
 
 // --------------------------------------------------------------------- softmax
 
-// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by the adder:
-// 1.5 2^23 + x), 2^f by the cubic that minimises the relative error on |f| <= 1/2 (7.5e-5,
-// by exchange; a weight is rounded to 2^-11 anyway), n added to the exponent.  Arguments
-// below -126 count as -126.
-__device__ __forceinline__ float2 ex2_cubic(float2 x) {
+// 2^x on the FMA pipe, of arguments limited to [-kCubicTop, kCubicTop]: a masked score counts as
+// the lower end, and one far above the reference must come out large, for the reference to be
+// moved, and not run over into the sign.  The saturation of the multiply-add that yields
+// y = (x / kCubicTop + 1) / 2 does both (minimum and maximum as instructions: a 2048-token
+// chunk at 16K 970 us against 960; d = 64 434 against 425).
+constexpr float kCubicTop = 126.0f;
+__device__ __forceinline__ float saturated(float a, float b, float c) {
+  float d;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// With x = n + r, n the nearest integer (by the adder: 1.5 2^23 + x), 2^r is the cubic that
+// minimises the relative error on |r| <= 1/2 (7.5e-5, by exchange; a weight is rounded to
+// 2^-11 anyway) and n is added to the exponent.
+__device__ __forceinline__ float2 ex2_cubic(float2 y) {
   constexpr float kMagic = 12582912.0f, c0 = 0.99992806f, c1 = 0.69326097f, c2 = 0.24261113f, c3 = 0.05517167f;
-  x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
-  const float2 t = add2(x, make_float2(kMagic, kMagic));
-  const float2 f = fma2(add2(t, make_float2(-kMagic, -kMagic)), make_float2(-1.0f, -1.0f), x);
-  float2 p = fma2(f, make_float2(c3, c3), make_float2(c2, c2));
-  p = fma2(p, f, make_float2(c1, c1));
-  p = fma2(p, f, make_float2(c0, c0));
+  const float2 span = make_float2(2.0f * kCubicTop, 2.0f * kCubicTop), from = make_float2(kMagic - kCubicTop, kMagic - kCubicTop);
+  const float2 t = fma2(y, span, from);
+  const float2 r = fma2(y, span, sub2(from, t));
+  float2 p = fma2(r, make_float2(c3, c3), make_float2(c2, c2));
+  p = fma2(p, r, make_float2(c1, c1));
+  p = fma2(p, r, make_float2(c0, c0));
   return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
@@ -444,10 +454,16 @@ struct Half {
       const float4 now = k;
       if (g + 1 < H / 16) k = sc[g + 1];
       const float f = factor(now.x, crow), off = now.y - m;
+      const float f_y = f * (0.5f / kCubicTop), off_y = fmaf(off, 0.5f / kCubicTop, 0.5f);
       float2 x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = fma2(make_float2(at(16 * g + 2 * i), at(16 * g + 2 * i + 1)), make_float2(f, f), make_float2(off, off));
+      for (int i = 0; i < 8; ++i) {
+        const float s0 = at(16 * g + 2 * i), s1 = at(16 * g + 2 * i + 1);
+        if (i * kCubic / 8 != (i + 1) * kCubic / 8)
+          x[i] = make_float2(saturated(s0, f_y, off_y), saturated(s1, f_y, off_y));
+        else
+          x[i] = fma2(make_float2(s0, s1), make_float2(f, f), make_float2(off, off));
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         x[i] = i * kCubic / 8 != (i + 1) * kCubic / 8 ? ex2_cubic(x[i]) : make_float2(ex2(x[i].x), ex2(x[i].y));

@@ -30,3 +30,32 @@ def test_late_scales_change_nothing(d, G, n):
     finally:
         _lib.set_test_hooks(0)
     assert torch.isfinite(good).all() and torch.equal(late, good)
+
+
+GAPS = [100.0, 120.0, 127.6, 128.2, 129.0, 130.0, 200.0, 256.0, 270.0, 400.0]
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("n", [20, 160])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_one_token_far_above_all_others(d, n, fmt):
+    """Flat scores but for one token, 2^GAPS[b] above them in sequence b and at place h of 16
+    tokens for kv head h, behind the first 64: its value is the output.  Its weight has 11 bits
+    and so has the row's sum against it (2^-11 each at most), the output is rounded once.  The
+    other 299 tokens weigh 2^-100 at most each, with values below 8: 299 * 8 * 2^-100 < 2^-88."""
+    require_cuda()
+    B, H, T = len(GAPS), 16, 300
+    c = BlockKVCache(B, H, d, T, block=16, dtype=fmt)
+    k = torch.zeros(B, H, T, d, device="cuda")
+    at = 80 + torch.arange(H)
+    k[:, torch.arange(H), at, 0] = 1.0
+    v = torch.randn(B, H, T, d, generator=torch.Generator("cuda").manual_seed(92), device="cuda")
+    c.append(k, v, i32([0] * B))
+    values = c.read(None, T, dtype=torch.float32)[1]
+    want = values[:, torch.arange(H), at][:, :, None].double()
+    q = torch.zeros(B, H, n, d, device="cuda", dtype=BF16)
+    q[..., 0] = torch.tensor(GAPS, device="cuda")[:, None, None].to(BF16)
+    got = c.attend(q, i32([T] * B), T, attn_scale=0.6931471805599453)
+    off = (got.double() - want).abs() > (2.0 ** -8 + 2.0 ** -10) * want.abs() + 2.0 ** -88
+    assert values.abs().max() < 8
+    assert not off.any(), sorted({(GAPS[b], int(h)) for b, h in off.nonzero()[:, :2].tolist()})
