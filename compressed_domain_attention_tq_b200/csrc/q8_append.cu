@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(1024, BF16 ? 1 : 0) append_kernel(Q8WriteArgs 
   valid = min(valid, a.n);
   const int64_t first = (int64_t)((pos >> block_shift) + j) << block_shift;  // the block's first row
   const int64_t stop = min((int64_t)pos + valid, c.capacity);
+  if (first >= stop) return;  // (the differences below then fit in 32 bits, wherever pos is)
   const int new0 = (int)max((int64_t)0, pos - first);           // new rows [new0, new1) of the block
   const int new1 = (int)min((int64_t)c.block, stop - first);
   if (new0 >= new1) return;

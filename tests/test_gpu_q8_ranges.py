@@ -59,3 +59,19 @@ def test_one_token_far_above_all_others(d, n, fmt):
     off = (got.double() - want).abs() > (2.0 ** -8 + 2.0 ** -10) * want.abs() + 2.0 ** -88
     assert values.abs().max() < 8
     assert not off.any(), sorted({(GAPS[b], int(h)) for b, h in off.nonzero()[:, :2].tolist()})
+
+
+@pytest.mark.parametrize("block", [16, 128])
+def test_appends_behind_the_capacity_wherever_they_begin(block):
+    """Places up to the last int32, with more tokens than the cache has rows: nothing is written."""
+    require_cuda()
+    c = BlockKVCache(4, 2, 64, 50, block=block)
+    x = torch.randn(4, 2, 300, 64, device="cuda")
+    c.append(x[:, :, :50].contiguous(), x[:, :, :50].contiguous(), i32([0] * 4))
+    before = [t.clone() for t in c.buffers[:4]]
+    for n in (1, 20, 100, 300):
+        y = (3 * x[:, :, :n]).contiguous()
+        c.append(y, y, i32([50, 2 ** 31 - n // 2 - 1, 2 ** 31 - n, 2 ** 31 - 1]))
+        c.append(y, y, i32([2 ** 31 - 1] * 4), n_valid=i32([n, 1, 2 ** 31 - 1, n // 2]))
+    for a, b in zip(before, c.buffers[:4]):
+        assert torch.equal(a, b)
