@@ -21,11 +21,12 @@
 //
 // Precision: codes are exact in f16.  Each query row is scaled by a power of
 // two and split into f16 hi + lo (22 bits; bf16 queries have no lo part), the
-// weights W = 2^(x - m) s_v / ref likewise, so a product costs two instructions
-// and keeps ~2^-22.  x = S s_k scale log2(e); m is a row's reference, moved only
-// when a score exceeds it by 2^8 (then W <= 2^15 stays in f16's range); ref is
-// the largest V scale so far, so W does not leave the range whatever the
-// scales are.  Sums of weights and O are fp32.
+// weights W = 2^(x - m) likewise, so a product costs two instructions and keeps
+// ~2^-22.  x = S s_k scale log2(e); m is a row's reference, moved only when a
+// score exceeds it by 2^8 (then W <= 2^15 stays in f16's range).  The V scales are
+// applied in fp32, to each step's sum as it is added, in units of ref, the largest
+// so far: in the weights a ratio s_v / ref of 1e-5 would already take bits from
+// their lo parts.  Sums of weights and O are fp32.
 //
 // Bound: HBM for decode (one pass over the codes).  Measured: d 256, 64K x 4
 // sequences, 32/16 heads 348 us, 94% of the measured copy rate; d 128, 32K x 8
@@ -142,7 +143,7 @@ struct Smem {
   // query fragments: hi pair 0, hi pair 1, and lo pair 0, lo pair 1 where queries have a lo part
   uint2 q[NT][D / 16][LO ? 2 : 1][32];
   float crow[8 * NT];               // scale of a row's sums: attn_scale log2(e) 2^-e
-  float m[kWarps][8 * NT], l[kWarps][8 * NT], ref[kWarps];
+  float m[kWarps][8 * NT], l[kWarps][8 * NT];
   union {
     alignas(16) unsigned char ring[kWarps][Ring<D, NT>::kSlots][Ring<D, NT>::kBytes];
     float acc[kWarps][8][D + 4];    // a row tile's sums of each warp (rows padded against bank conflicts)
@@ -362,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         const float mm = m[nt][j & 1] == -INFINITY ? 0.0f : m[nt][j & 1];
         p[j] = tc::ex2(x[j] - mm);
         l[nt][j & 1] += p[j];
-        p[j] *= ratio;
       }
       uint32_t h0, l0, h1, l1;
       split2(p[0], p[1], h0, l0);
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
           mma(o, f, wlo[nt][0], wlo[nt][1]);
           mma(o, f, whi[nt][0], whi[nt][1]);
           float(&sum)[4] = acc[nt][2 * w + h];
-          const float2 s0 = add2(make_float2(sum[0], sum[1]), make_float2(o[0], o[1]));
-          const float2 s1 = add2(make_float2(sum[2], sum[3]), make_float2(o[2], o[3]));
+          const float2 s0 = fma2(make_float2(o[0], o[1]), make_float2(ratio, ratio), make_float2(sum[0], sum[1]));
+          const float2 s1 = fma2(make_float2(o[2], o[3]), make_float2(ratio, ratio), make_float2(sum[2], sum[3]));
           sum[0] = s0.x, sum[1] = s0.y, sum[2] = s1.x, sum[3] = s1.y;
         }
       }

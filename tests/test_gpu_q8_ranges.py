@@ -1,14 +1,31 @@
 """The 8-bit block-scaled cache on the GPU where values, places and timing are far from ordinary:
 scores and scales far apart, places near the ends of int32, warps that come late.  The reference
 and the gates of test_gpu_q8.py, tighter where a test says so."""
+import math
+
 import pytest
 import torch
 
 from compressed_domain_attention_tq_b200 import BlockKVCache, _lib
 from conftest import require_cuda
-from test_gpu_q8 import BF16, i32
+from test_gpu_q8 import BF16, F32, i32
 
 pytestmark = pytest.mark.gpu
+
+
+def definition(c, q, ctx, scale):
+    """Attention of q [B][Hq][n][d] over the cache's values in 64 bits, every sequence of length ctx
+    -> (outputs, the weights' sum of |v|, the largest score and the logarithm of the sum of weights in
+    powers of two)."""
+    k, v = (x.double() for x in c.read(None, ctx, dtype=F32))
+    B, Hq, n, d = q.shape
+    H = c.num_kv_heads
+    s = (q.double().view(B, H, -1, d) @ k.transpose(-1, -2)).view(B, H, -1, n, ctx) * scale
+    last = torch.arange(n, device="cuda") + ctx - n
+    s.masked_fill_(torch.arange(ctx, device="cuda") > last[:, None], -torch.inf)
+    p = torch.softmax(s, -1).view(B, H, -1, ctx)
+    top, lse = s.amax(-1) / math.log(2), torch.logsumexp(s, -1) / math.log(2)
+    return ((p @ v).view(B, Hq, n, d), (p @ v.abs()).view(B, Hq, n, d), top.view(B, Hq, n), lse.view(B, Hq, n))
 
 
 @pytest.mark.parametrize("d,G,n", [(128, 4, 64), (128, 8, 8), (256, 4, 40), (64, 4, 64), (96, 2, 100), (64, 8, 4)])
@@ -75,3 +92,33 @@ def test_appends_behind_the_capacity_wherever_they_begin(block):
         c.append(y, y, i32([2 ** 31 - 1] * 4), n_valid=i32([n, 1, 2 ** 31 - 1, n // 2]))
     for a, b in zip(before, c.buffers[:4]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_fp32_rows_behind_a_huge_block_keep_their_precision(d, n):
+    """The first block's V is 1e5 to 1e20 times the others' and its keys score 69 nats below
+    them, so that it adds nothing (e^-69 2^66 = 1e-10).  384 heads: a work item holds a whole context.
+    fp32 queries: a score's error is 2^-20 of scale sum |q k| (22 bits of a query element, d / 16 sums in
+    the tensor cores), a weight's that and 2^-20 for its exponent and its two parts; the outputs'
+    twice a weight's of the weighted |v|."""
+    require_cuda()
+    B, H, T = 12, 32, 400
+    g = torch.Generator("cuda").manual_seed(93)
+    c = BlockKVCache(B, H, d, T, block=64)
+    k, v = (torch.randn(B, H, T, d, generator=g, device="cuda") for _ in range(2))
+    k[..., 0] = 0
+    k[:, :, :64] = 0
+    k[:, :, :64, 0] = -1
+    v[:, :, :64] *= torch.tensor([1e5, 1e7, 1e10, 1e20], device="cuda").repeat(3)[:, None, None, None]
+    c.append(k, v, i32([0] * B))
+    q = torch.randn(B, 2 * H, n, d, generator=g, device="cuda")
+    scale = d ** -0.5
+    q[..., 0] = 69 / scale
+    c.v_codes[1, :, :64] = 0  # (one sequence whose first block only has a large scale)
+    want, size, *_ = definition(c, q, T, scale)
+    got = (c.attend(q, i32([T] * B), T) if n > 1 else c.decode(q[:, :, 0].contiguous(), i32([T] * B), T)[:, :, None])
+    kk = c.read(None, T, dtype=F32)[0][:, :, 64:].abs().double().repeat_interleave(2, 1)
+    spread = scale * (q.abs().double() @ kk.transpose(-1, -2)).amax(-1, keepdim=True)
+    off = (got.double() - want).abs() > 2 * 2.0 ** -20 * (spread + 1) * size
+    assert not off.any(), off.sum((1, 2, 3)).tolist()
