@@ -141,6 +141,14 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return d;
 }
 
+// The exponent of a sum of weights (0 for sums of 0 and NaN).  States (m, l) and outputs are
+// written divided by 2^this, with m raised by it: l is then in [1, 2), m within one of the
+// logarithm of the sum, and an output no larger than twice the largest value.
+__device__ __forceinline__ int sum_exponent(float l) {
+  const int e = (int)(__float_as_uint(l) >> 23);
+  return e == 0 || e >= 255 ? 0 : e - 127;
+}
+
 // Division by the block's scale s, correctly rounded: with r = RN(1/s), two
 // residual steps q <- q + r (x - q s) end on RN(x / s) (Markstein's theorem:
 // the last step starts from a faithful quotient and the residual of a fused

@@ -404,15 +404,18 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge starts and waits for this grid
 
   // -- join the warps: sums over the lanes of a row, then over the warps
+  float down[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
+      const int e = sum_exponent(l[nt][k]);
+      down[nt][k] = tc::pow2i(-e);
       if (g == 0) {
-        sm.m[warp][8 * nt + 2 * t + k] = m[nt][k];
-        sm.l[warp][8 * nt + 2 * t + k] = l[nt][k];
+        sm.m[warp][8 * nt + 2 * t + k] = m[nt][k] + (float)e;
+        sm.l[warp][8 * nt + 2 * t + k] = l[nt][k] * down[nt][k];
       }
     }
 #pragma unroll
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int byte = 2 * i + (j >> 1);  // byte of this lane's part of a V row
-        sm.acc[warp][2 * t + (j & 1)][v_offset<D>(byte >> 2, g) + (byte & 3)] = acc[nt][i][j] * ref;
+        sm.acc[warp][2 * t + (j & 1)][v_offset<D>(byte >> 2, g) + (byte & 3)] = acc[nt][i][j] * down[nt][j & 1] * ref;
       }
     __syncthreads();
     for (int p = threadIdx.x; p < 8 * (D / 4); p += kThreads) {

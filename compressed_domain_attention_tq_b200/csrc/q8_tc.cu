@@ -37,7 +37,7 @@
 //
 // Bound: for long chunks the exponentials and the products in turn (the softmax of one
 // row tile overlaps the other's products, 41% to 49% of the tensor cores' time each):
-// 2048 tokens of 64/8 heads at 16K, d 128, 960 us = 1.07 PFLOP/s, 65% of the measured
+// 2048 tokens of 64/8 heads at 16K, d 128, 951 us = 1.08 PFLOP/s, 65% of the measured
 // matrix-product rate; d 256 (32/16 heads, 1024 tokens at 8K) 258 us = 1.00; d 96 260 us
 // = 0.69 and d 64 425 us = 0.57, whose products are shorter per exponential.  For few rows
 // the chain of products and softmax of a token tile, 2100 clocks where HBM would need
@@ -565,7 +565,17 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
   const int64_t orow = it.out_row(a, local);
   const bool split = it.split;
   if (*abort) l = __int_as_float(0x7fc00000);
-  const float f = none ? 0.0f : split ? ref : ref / l;
+  const int e = sum_exponent(l);
+  const float down = pow2i(-e);
+  m += (float)e;
+  l *= down;
+  float f = split ? down : down / l;
+  if (__any_sync(0xffffffffu, f * ref < 0x1p-100f)) {  // O by parts, where the product might lose bits
+    rescale<D>(tbase + lanes + L::O(ou), f);
+    wait_st();
+    f = 1.0f;
+  }
+  f *= ref;
   float* part = it.part(a, local, MODE == kQ8TwoStreams ? u : 0);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {

@@ -617,9 +617,10 @@ TQ_API size_t tq_sdpa_q8_workspace_bytes(int32_t batch, int32_t num_q_heads, int
  *            long query chunks may be computed with weights of 11 bits (an
  *            error well below that of the output's own rounding).
  *  lse       NULL, or float [B][Hq][n_q][2], 8-byte aligned: (M, L) with
- *            L = sum_t 2^(attn_scale * q.k_t * log2(e) - M), M near the maximum
- *            (-inf and 0 where nothing is attended).  With n_q = 1 and fp32
- *            outputs these are parts for tq_merge_lse.
+ *            L = sum_t 2^(attn_scale * q.k_t * log2(e) - M), M between one below
+ *            the largest exponent and the logarithm of the sum of all (-inf and
+ *            0 where nothing is attended).  With n_q = 1 and fp32 outputs these
+ *            are parts for tq_merge_lse.
  *  workspace tq_sdpa_q8_workspace_bytes() bytes, 16-byte aligned.
  * Errors as tq_sdpa_int4_decode.
  */

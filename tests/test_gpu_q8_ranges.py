@@ -122,3 +122,51 @@ def test_fp32_rows_behind_a_huge_block_keep_their_precision(d, n):
     spread = scale * (q.abs().double() @ kk.transpose(-1, -2)).amax(-1, keepdim=True)
     off = (got.double() - want).abs() > 2 * 2.0 ** -20 * (spread + 1) * size
     assert not off.any(), off.sum((1, 2, 3)).tolist()
+
+
+def filled(B, H, T, d, seed, size=1.0, block=64, positive=False):
+    """A cache of normal draws, V (or |V|) times size (a number, or a tensor that broadcasts)."""
+    require_cuda()
+    g = torch.Generator("cuda").manual_seed(seed)
+    c = BlockKVCache(B, H, d, T, block=block)
+    k, v = (torch.randn(B, H, T, d, generator=g, device="cuda") for _ in range(2))
+    c.append(k, (v.abs() if positive else v) * size, i32([0] * B))
+    return c, g
+
+
+@pytest.mark.parametrize("dtype,n", [(F32, 1), (F32, 9), (BF16, 20), (BF16, 160)])
+@pytest.mark.parametrize("B,H", [(1, 2), (5, 32)])
+def test_softmax_states_are_near_the_maximum(B, H, dtype, n):
+    """lse = (M, L): M lies between one below the largest score and the logarithm of the sum, also where
+    the row sees only blocks whose V is small beside another's; few heads (joined parts) and many
+    (whole contexts).  M + log2(L) is the logarithm: scores of 11-bit queries, fp32 sums (4e-3 in bf16,
+    whose weights have 11 bits of their own, as elsewhere)."""
+    T, d = 1100, 128
+    size = torch.ones(T, 1, device="cuda")
+    size[:512] = 1e-20
+    size[512:1024] = 1e-36
+    c, g = filled(B, H, T, d, 94, size, block=16)
+    q = torch.randn(B, 2 * H, n, d, generator=g, device="cuda").to(dtype)
+    lse = torch.empty(B, 2 * H, n, 2, device="cuda")
+    for ctx in (T, 1024, 512):
+        _, _, top, want = definition(c, q, ctx, d ** -0.5)
+        c.attend(q, i32([ctx] * B), T, lse=lse)
+        M, L = lse.double().unbind(-1)
+        assert ((M + torch.log2(L)) - want).abs().max() < (4e-3 if dtype == BF16 else 1e-4)
+        assert (M > top - 1.01).all() and (M < want + 0.01).all(), (ctx, (M - top).min(), (M - want).max())
+
+
+@pytest.mark.parametrize("size", [3e33, 1e-36])
+@pytest.mark.parametrize("dtype,n", [(F32, 1), (F32, 9), (BF16, 20), (BF16, 160)])
+@pytest.mark.parametrize("B,H,T,d", [(1, 2, 3000, 128), (5, 32, 4096, 64), (5, 32, 500, 256)])
+def test_values_near_the_ends_of_the_range(B, H, T, d, dtype, n, size):
+    """Sums of weights times V stay in fp32's range and keep its bits, positive as they are here.
+    Tolerances of the fp32 rows behind a huge block (scores of normal draws: scale sum |q k| < 32) and
+    of bf16 outputs, and half of bf16's last place below its normal numbers, 2^-134."""
+    c, g = filled(B, H, T, d, 95, size, positive=True)
+    q = (0.5 * torch.randn(B, H, n, d, generator=g, device="cuda")).to(dtype)
+    got = c.attend(q, i32([T] * B), T).double()
+    want, weighted, *_ = definition(c, q, T, d ** -0.5)
+    tol = 2 * 2.0 ** -20 * 33 * weighted if dtype == F32 else 2.0 ** -8 * want.abs() + 2.0 ** -10 * weighted
+    off = (got - want).abs() > tol + 2.0 ** -134
+    assert torch.isfinite(got).all() and not off.any(), (off.sum().item(), off.numel())
