@@ -556,7 +556,7 @@ __device__ __forceinline__ void softmax_role(const Q8AttendArgs& a, int begin, i
   if (nt > 0) warp_wait(bar + kDone, 0, abort);
   fence_after();
   if (!warp_live) return;
-  const bool none = n == 0 || (m == -INFINITY && l < 1e-20f);  // (masked weights of the cubic are 2^-126)
+  const bool none = n == 0 || (m == -INFINITY && l == l);  // (masked weights of the cubic are 2^-126, not 0)
   if (none) l = 0.0f;
   // where the row goes, worked out anew rather than kept in registers through the loop
   int id;

@@ -170,3 +170,22 @@ def test_values_near_the_ends_of_the_range(B, H, T, d, dtype, n, size):
     tol = 2 * 2.0 ** -20 * 33 * weighted if dtype == F32 else 2.0 ** -8 * want.abs() + 2.0 ** -10 * weighted
     off = (got - want).abs() > tol + 2.0 ** -134
     assert torch.isfinite(got).all() and not off.any(), (off.sum().item(), off.numel())
+
+
+@pytest.mark.parametrize("n", [20, 160])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_states_of_queries_that_attend_nothing(d, n):
+    """Positions below 0, in tiles whose other tokens have blocks of zero V: (-inf, 0) and zeros, as of
+    every row that attends nothing; 160 heads, so that contexts are not split."""
+    B, H = 5, 32
+    size = torch.ones(64, 1, device="cuda")
+    size[16:] = 0
+    c, g = filled(B, H, 64, d, 96, size, block=16)
+    q = torch.randn(B, H, n, d, generator=g, device="cuda", dtype=BF16)
+    for ctx in (5, 0, 19):
+        lse = torch.full((B, H, n, 2), 5.0, device="cuda")
+        got = c.attend(q, i32([ctx] * B), 64, lse=lse)
+        none = max(0, n - ctx)
+        assert torch.all(got[:, :, :none] == 0)
+        assert torch.all(lse[:, :, :none, 0] == -torch.inf) and torch.all(lse[:, :, :none, 1] == 0)
+        assert torch.all(lse[:, :, none:, 1] >= 1)
