@@ -141,6 +141,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return d;
 }
 
+// The power of two by which a query row is multiplied: its largest element comes into
+// [2^13, 2^14), as far as 2^e and 2^-e are normal numbers (every finite row stays below 2^16).
+__device__ __forceinline__ int query_exponent(float top) {
+  return top > 0.0f ? max(-114, min(126, 13 - ilogbf(top))) : 0;
+}
+
 // The exponent of a sum of weights (0 for sums of 0 and NaN).  States (m, l) and outputs are
 // written divided by 2^this, with m raised by it: l is then in [1, 2), m within one of the
 // logarithm of the sum, and an output no larger than twice the largest value.

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
       for (int x = lane; x < D; x += 32) top = fmaxf(top, fabsf(q_elem(a, qrow, x)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+    const int e = query_exponent(top);
     const float up = tc::pow2i(e);
     const int nt = r >> 3, rg = r & 7;
     for (int p = lane; p < KW * 4; p += 32) {  // (word, lane of 4)

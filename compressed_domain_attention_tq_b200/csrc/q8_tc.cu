@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const Q8AttendArgs a) {
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      const int e = big > 0.0f ? max(-100, min(100, 13 - ilogbf(big))) : 0;
+      const int e = query_exponent(big);
       const float up = pow2i(e);
       unsigned char* dst = smem + L::Q + (r >> 7) * L::Q_BYTES + ((r ^ L::kRowFlip) & 127) * 16;
 #pragma unroll
