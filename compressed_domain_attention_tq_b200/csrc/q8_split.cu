@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
           for (int j = 0; j < 4; ++j) acc[nt][i][j] *= down;
       ref = vs;
     }
-    const float ratio = ref > 0.0f ? vs / ref : 0.0f;
+    const float ratio = vs == ref ? 1.0f : vs / ref;
     uint32_t whi[NT][2], wlo[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
