@@ -56,6 +56,15 @@ struct Piece {
       for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
     }
   }
+  // signs of elements 4 half .. 4 half + 3 in the top bits of the bytes
+  __device__ __forceinline__ uint32_t signs(int half) const {
+    if constexpr (BF16) {
+      return (half ? tc::prmt(w[0].z, w[0].w, 0x7531) : tc::prmt(w[0].x, w[0].y, 0x7531)) & 0x80808080u;
+    } else {
+      const uint4 u = w[half];
+      return tc::prmt(tc::prmt(u.x, u.y, 0x0073), tc::prmt(u.z, u.w, 0x0073), 0x5410) & 0x80808080u;
+    }
+  }
   // Running maximum of the bits of |x|: two 16-bit lanes for bf16, one word for fp32.
   __device__ __forceinline__ void max_bits(uint32_t& top) const {
     if constexpr (BF16) {
@@ -170,8 +179,12 @@ __global__ void __launch_bounds__(1024, BF16 ? 1 : 0) append_kernel(Q8WriteArgs 
       x[i].values(v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = div.quick(v[e]);
-      if (whole || (p >= lo && p < hi))
-        *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = make_uint2(F::codes4(v[0], v[1]), F::codes4(v[2], v[3]));
+      uint2 code = make_uint2(F::codes4(v[0], v[1]), F::codes4(v[2], v[3]));
+      if constexpr (F::kSignedZero) {  // the division's residual steps turn -0 into +0
+        code.x |= x[i].signs(0);
+        code.y |= x[i].signs(1);
+      }
+      if (whole || (p >= lo && p < hi)) *reinterpret_cast<uint2*>(codes + (int64_t)p * 8) = code;
     }
   } else {
 #pragma unroll 1

@@ -55,6 +55,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 struct Int8 {
   static constexpr float kMax = 127.0f;
+  static constexpr bool kSignedZero = false;
   // byte place of a 32-bit word that cvt_word puts into half k of pair p
   static __host__ __device__ constexpr int place(int p, int k) { return p + 2 * k; }
 
@@ -94,6 +95,7 @@ struct Int8 {
 
 struct E4m3 {
   static constexpr float kMax = 448.0f;
+  static constexpr bool kSignedZero = true;
   static __host__ __device__ constexpr int place(int p, int k) { return 2 * p + k; }
 
   static __device__ __forceinline__ uint32_t cvt2(uint32_t two) {

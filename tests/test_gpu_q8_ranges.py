@@ -209,3 +209,24 @@ def test_queries_near_the_ends_of_the_range(d, dtype, n, size):
         tol = tol + 2.0 ** -8 * want.abs() + 2.0 ** -10 * weighted
     off = ~((got - want).abs() <= tol)
     assert not off.any(), (off.sum().item(), off.numel())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+def test_append_keeps_the_sign_of_zeros(d, fmt):
+    """Codes are those of fl32(x / s) bit for bit: an e4m3 code of -0 is 0x80, in a block that has an
+    infinity as in one that has not (int8 has one zero)."""
+    require_cuda()
+    for dtype in (F32, BF16):
+        c = BlockKVCache(1, 2, d, 64, block=16, dtype=fmt)
+        x = torch.randn(1, 2, 64, d, device="cuda").to(dtype)
+        x[..., ::3] = -0.0
+        x[..., 1::3] = 0.0
+        x[:, :, 20, 2], x[:, :, 21, 5] = torch.inf, -torch.inf
+        x[:, :, 40, 2] = -1e-44  # underflows against the block's scale
+        c.append(x, x, i32([0]))
+        zero = x == 0
+        want = torch.where(torch.signbit(x) & (fmt != torch.int8), 0x80, 0).to(torch.uint8)
+        codes = c.k_codes.view(torch.uint8)
+        assert torch.equal(codes[zero], want[zero]) and torch.equal(codes, c.v_codes.view(torch.uint8))
+        assert (codes[:, :, 40, 2] == (0 if fmt == torch.int8 else 0x80)).all()
