@@ -219,7 +219,9 @@ tq_status tq_read_q8(const void* k_codes, const float* k_scales, const void* v_c
     return TQ_ERR_INVALID_ARG;
   if (misaligned(k_out, 16) || misaligned(v_out, 16) || misaligned(pos, 4) || misaligned(n_valid, 4))
     return TQ_ERR_INVALID_ARG;
-  if (2 * (int64_t)batch * num_kv_heads * ((int64_t)rows / 16 + 1) > INT32_MAX) return TQ_ERR_INVALID_ARG;
+  // (a CTA takes 16 to 128 rows; row numbers are rounded up to those in 32 bits)
+  if (2 * (int64_t)batch * num_kv_heads * ((int64_t)rows / 16 + 1) > INT32_MAX || rows > INT32_MAX - 128)
+    return TQ_ERR_INVALID_ARG;
   a.k = k_out;
   a.v = v_out;
   a.bf16 = out_dtype == TQ_BF16;
