@@ -677,6 +677,12 @@ def _q8_lens(B, **lens):
             raise ValueError(f"{name} must be int32 [B]")
 
 
+def _q8_ctx(max_ctx, cap, where):
+    """What the library checks of max_ctx too, before ctypes takes its low 32 bits."""
+    if not 0 < max_ctx <= min(cap, (1 << 31) - 1):
+        raise TQError(TQ_ERR_INVALID_ARG, where)
+
+
 class _Here:
     """The current stream of the current device: nothing to switch to."""
 
@@ -763,6 +769,8 @@ def read_q8(k_codes, k_scales, v_codes, v_scales, block, pos, rows, n_valid=None
 
 def sdpa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx,
                             dtype=torch.float32) -> int:
+    if max(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx) >= 1 << 31:
+        return 0
     return int(load().tq_sdpa_q8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, n_q, max_ctx,
                                                  _dtype_of(dtype)))
 
@@ -801,6 +809,7 @@ def sdpa_q8(q, k_codes, k_scales, v_codes, v_scales, block, ctx_lens, max_ctx, q
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
         raise ValueError("q must be [B][Hq][n][d]")
     _q8_lens(B, ctx_lens=ctx_lens, q_lens=q_lens)
+    _q8_ctx(max_ctx, cap, "tq_sdpa_q8")
     Hq, n = q.shape[1], q.shape[2]
     with _launch(device, stream) as s:
         out = _q8_out(out, lse, q, q.dtype, zero=q_lens is not None)
@@ -825,6 +834,7 @@ def sdpa_q8_decode(q, k_codes, k_scales, v_codes, v_scales, block, ctx_lens, max
     if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
         raise ValueError("q must be [B][Hq][d]")
     _q8_lens(B, ctx_lens=ctx_lens)
+    _q8_ctx(max_ctx, cap, "tq_sdpa_q8")
     Hq = q.shape[1]
     with _launch(device, stream) as s:
         out = _q8_out(out, lse, q, torch.float32)
@@ -853,6 +863,7 @@ def sdpa_q8_decode_append(q, k_new, v_new, k_codes, k_scales, v_codes, v_scales,
     if k_new.dtype != v_new.dtype:
         raise TypeError("k_new and v_new must share dtype")
     _q8_lens(B, ctx_lens=ctx_lens)
+    _q8_ctx(max_ctx, cap, "tq_sdpa_q8_decode_append")
     Hq = q.shape[1]
     with _launch(device, stream) as s:
         out = _q8_out(out, lse, q, torch.float32)

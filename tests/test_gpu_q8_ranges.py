@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from compressed_domain_attention_tq_b200 import BlockKVCache, _lib
+from compressed_domain_attention_tq_b200 import BlockKVCache, TQError, _lib
 from conftest import require_cuda
 from test_gpu_q8 import BF16, F32, i32
 
@@ -230,3 +230,15 @@ def test_append_keeps_the_sign_of_zeros(d, fmt):
         codes = c.k_codes.view(torch.uint8)
         assert torch.equal(codes[zero], want[zero]) and torch.equal(codes, c.v_codes.view(torch.uint8))
         assert (codes[:, :, 40, 2] == (0 if fmt == torch.int8 else 0x80)).all()
+
+
+def test_lengths_beyond_the_cache_are_refused():
+    """max_ctx is compared with the capacity as it is given, not by its low 32 bits."""
+    c, _ = filled(1, 2, 40, 64, 98)
+    x, one = torch.zeros(1, 2, 1, 64, device="cuda"), i32([1])
+    for size in (41, 0, -1, (1 << 32) + 40, 1 << 31, 1 << 40):
+        for f in (lambda: c.decode(x[:, :, 0], one, size), lambda: c.attend(x, one, size),
+                  lambda: c.decode_append(x[:, :, 0], x, x, one, size)):
+            with pytest.raises(TQError) as e:
+                f()
+            assert e.value.status == _lib.TQ_ERR_INVALID_ARG
