@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from compressed_domain_attention_tq_b200 import BlockKVCache, TQError, _lib
+from compressed_domain_attention_tq_b200 import BlockKVCache, TQError, _lib, context_parallel
 from conftest import require_cuda
 from test_gpu_q8 import BF16, F32, i32
 
@@ -242,3 +242,33 @@ def test_lengths_beyond_the_cache_are_refused():
             with pytest.raises(TQError) as e:
                 f()
             assert e.value.status == _lib.TQ_ERR_INVALID_ARG
+
+
+def test_context_parallel_decode_takes_a_block_cache():
+    """One rank's shard is the whole context: the call is decode and the merge of one part."""
+    c, g = filled(2, 2, 700, 128, 99)
+    q = torch.randn(2, 16, 128, generator=g, device="cuda", dtype=BF16)
+    got = context_parallel.decode(c, q, i32([700, 300]), 700)
+    torch.testing.assert_close(got, c.decode(q, i32([700, 300]), 700), rtol=2.0 ** -21, atol=0)
+
+
+def test_long_sums_of_positive_values_keep_their_last_bits():
+    """fp32 decode of positive values over 64K tokens, d = 256: each warp adds 256 and more steps.  Rounding
+    to nearest, an addition is off by at most 2^-24 of a sum that grows evenly: 256 such errors come to
+    256^(1/2) 2^-24 / 3^(1/2) < 2^-20.8 in the mean square, and six times that below 2^-18.  Cut off
+    instead they add up to 256 2^-24 / 2 = 2^-17 on average."""
+    require_cuda()
+    B, H, T, d = 4, 16, 65536, 256
+    c = BlockKVCache(B, H, d, T, block=128)
+    g = torch.Generator("cuda").manual_seed(100)
+    for at in range(0, T, 8192):
+        k, v = (torch.randn(B, H, 8192, d, generator=g, device="cuda", dtype=BF16) for _ in range(2))
+        c.append(k, v.abs(), i32([at] * B))
+    q = torch.randn(B, 2 * H, d, generator=g, device="cuda")
+    got = c.decode(q, i32([T] * B), T).double()
+    for b in range(B):
+        for h in range(H):
+            k, v = ((x[b, h].double() * s[b, h].double().repeat_interleave(128)[:, None])
+                    for x, s in ((c.k_codes, c.k_scales), (c.v_codes, c.v_scales)))
+            want = torch.softmax(q[b, 2 * h:2 * h + 2].double() @ k.T / 16, -1) @ v
+            assert ((got[b, 2 * h:2 * h + 2] / want - 1).abs().max() < 2.0 ** -18)
