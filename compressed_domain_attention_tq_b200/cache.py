@@ -336,8 +336,11 @@ class UniformKVCache(CodebookKVCache):
 
 class BlockKVCache:
     """The 8-bit block-scaled cache: int8 or e4m3 codes with one fp32 scale for each block of
-    tokens of a kv head, unrotated (q8 in include/tq.h).  The calls of Int4KVCache, and
-    attend() for several query tokens per sequence (a prefill chunk, drafted tokens).
+    tokens of a kv head, unrotated (q8 in include/tq.h).  append, decode, decode_lse,
+    decode_append and dequantize as Int4KVCache has them, read() of any range, and attend()
+    for several query tokens per sequence (a prefill chunk, drafted tokens).  The bound and
+    host-buffer calls of Int4KVCache and its workspace() are not offered; the size of a
+    workspace is sdpa_q8_workspace_bytes().
 
     head_dim 64, 96, 128 or 256; block 16, 32, 64 or 128 tokens; dtype torch.int8 or
     torch.float8_e4m3fn.  Calls use no state but the codes and scales: each allocates its

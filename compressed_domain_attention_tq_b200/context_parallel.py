@@ -57,8 +57,8 @@ def decode(cache, q: torch.Tensor, ctx_lens: torch.Tensor, max_ctx: int,
            stream=None) -> torch.Tensor:
     """Attention of q [B][Hq][d] over the union of every rank's shard.
 
-    cache      this rank's Int4KVCache or CodebookKVCache (its shard, rows 0 .. ctx_lens[b]-1);
-               every rotation and code format the caches support.
+    cache      this rank's Int4KVCache, CodebookKVCache or BlockKVCache (its shard, rows
+               0 .. ctx_lens[b]-1); every rotation and code format the caches support.
     ctx_lens   this rank's shard lengths (device int32 [B], each >= 1).
     max_ctx    host bound on this rank's ctx_lens.
     Every rank calls this with the same q, attn_scale and group; every rank

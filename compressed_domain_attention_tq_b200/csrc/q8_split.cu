@@ -16,8 +16,8 @@
 // A warp copies its own steps into a ring of its own in shared memory
 // (cp.async), two steps ahead of the one it computes: no barrier is on the way,
 // and the copies cost no registers.  Loads straight into the lanes' registers,
-// one step ahead, waited for HBM in every step (128K, 64/8 heads, d 128: 62 us
-// against 60; d 256, 64K, 4 sequences: 408 against 356).
+// one step ahead, waited for HBM in every step (side by side: 128K, 64/8 heads, d 128
+// 62 us against 60; d 256, 64K, 4 sequences 408 against 356).
 //
 // Precision: codes are exact in f16.  Each query row is scaled by a power of
 // two and split into f16 hi + lo (22 bits; bf16 queries have no lo part), the
@@ -28,10 +28,10 @@
 // so far: in the weights a ratio s_v / ref of 1e-5 would already take bits from
 // their lo parts.  Sums of weights and O are fp32.
 //
-// Bound: HBM for decode (one pass over the codes).  Measured: d 256, 64K x 4
-// sequences, 32/16 heads 348 us, 94% of the measured copy rate; d 128, 32K x 8
-// sequences, 64/8 heads 103 us, 79%; 128K of one sequence 56 us, 72%, about 15 us
-// of it launches, the first step's latency and the merge.  Tiles of 16 rows
+// Bound: HBM for decode (one pass over the codes).  Measured (int8, bf16 queries, captured
+// calls repeated on one input): d 256, 64K x 4 sequences, 32/16 heads 357 us, 91% of the
+// measured copy rate; d 128, 32K x 8 sequences, 64/8 heads 108 us, 76%; 128K of one
+// sequence 61 us, 67%, about 15 us of it launches, the first step's latency and the merge.  Tiles of 16 rows
 // (NT = 2) convert a code once for two products; they are taken when a kv head
 // has more than 8 rows.
 #include <limits.h>

@@ -37,11 +37,13 @@
 //
 // Bound: for long chunks the exponentials and the products in turn (the softmax of one
 // row tile overlaps the other's products, 41% to 49% of the tensor cores' time each):
-// 2048 tokens of 64/8 heads at 16K, d 128, 951 us = 1.08 PFLOP/s, 65% of the measured
-// matrix-product rate; d 256 (32/16 heads, 1024 tokens at 8K) 258 us = 1.00; d 96 260 us
-// = 0.69 and d 64 425 us = 0.57, whose products are shorter per exponential.  For few rows
+// 2048 tokens of 64/8 heads at 16K, d 128, int8, normal draws, 953 us = 1.08 PFLOP/s, 65%
+// of the measured matrix-product rate (e4m3 921 us; keys and values with outliers, where
+// the reference moves more often, 1050 us); d 256 (32/16 heads, 1024 tokens at 8K) 260 us
+// = 0.99; d 96 (32/32, 2048 at 8K) 263 us = 0.68 and d 64 (2 x 32/8, 2048 at 8K) 426 us
+// = 0.56, whose products are shorter per exponential.  For few rows
 // the chain of products and softmax of a token tile, 2100 clocks where HBM would need
-// 1420: 5 drafted tokens at 128K 84 us, 3.2 TB/s.
+// 1420: 5 drafted tokens at 128K 82 us, 3.3 TB/s.
 #include <limits.h>
 #include <math.h>
 
