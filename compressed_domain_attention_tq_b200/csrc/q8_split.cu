@@ -21,12 +21,13 @@
 //
 // Precision: codes are exact in f16.  Each query row is scaled by a power of
 // two and split into f16 hi + lo (22 bits; bf16 queries have no lo part), the
-// weights W = 2^(x - m) likewise, so a product costs two instructions and keeps
-// ~2^-22.  x = S s_k scale log2(e); m is a row's reference, moved only when a
-// score exceeds it by 2^8 (then W <= 2^15 stays in f16's range).  The V scales are
-// applied in fp32, to each step's sum as it is added, in units of ref, the largest
-// so far: in the weights a ratio s_v / ref of 1e-5 would already take bits from
-// their lo parts.  Sums of weights and O are fp32.
+// weights W = 2^(x - m) s_v / 2^E likewise, so a product costs two instructions and
+// keeps ~2^-22.  x = S s_k scale log2(e); E is the exponent of the largest V scale so
+// far; m is a row's reference, moved only when a W comes near 2^15.  It is taken from
+// x and s_v together, so the tokens that make up the output have their bits, whether
+// by their weight or by their values: with m from x alone the weights of a block of V
+// 1e5 times the others' and 14 nats below them came near f16's smallest number.  When
+// E grows m falls with it, and O stays as it is.  Sums of weights and O are fp32.
 //
 // Bound: HBM for decode (one pass over the codes).  Measured (int8, bf16 queries, captured
 // calls repeated on one input): d 256, 64K x 4 sequences, 32/16 heads 357 us, 91% of the
@@ -46,8 +47,12 @@ namespace {
 using namespace q8;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kStep = 16;
-constexpr float kTau = 8.0f;    // how far (log2) a score may exceed the reference
-constexpr float kShift = 7.0f;  // weights are kept 2^kShift larger: 2^(kTau + kShift) < 65504
+constexpr float kTau = 7.0f;    // how far (log2) a weight may exceed the reference
+constexpr float kShift = 7.0f;  // weights are kept 2^kShift larger: W < 2^(kTau + kShift + 1)
+// V scales count as no further than 2^kSpan apart in m, so that sums of 2^(x - m) stay in
+// fp32's range (2^(kTau + kShift + kSpan) a token); those of blocks of zeros, which add to the
+// sum of weights alone, as 2^-kZeroSpan of the largest
+constexpr int kSpan = 90, kZeroSpan = 45, kNoScale = -1000;
 
 // Byte offsets in a row of d codes.  K: word w (0 .. d/16 - 1) of lane t of 4;
 // V: word w (0 .. d/32 - 1) of lane g of 8.  Whole 16-byte loads where d allows.
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.0f;
-  float ref = 0.0f;
+  int ref = kNoScale, span = 0;  // E, and how far below it V scales have been
 
   for (; tok < stop; tok += kStep * kWarps) {
     asm volatile("cp.async.wait_group %0;" ::"n"(R::kSlots - 2) : "memory");
@@ -313,17 +318,30 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
       }
     }
 
-    if (vs > ref) {  // warp-uniform: a larger V scale becomes the reference
-      const float down = ref / vs;
+    const bool some = vs != 0.0f;  // (warp-uniform, as all of this)
+    const int ve = max(-126, min(126, (int)(__float_as_uint(vs) >> 23) - 127));
+    if (some && ve > ref) {
+      const int low = ref == kNoScale ? span : min(ve - ref, kSpan - span);
+      const float up = tc::pow2i(low), down = tc::pow2i(max(low - (ve - ref), -126));
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int k = 0; k < 2; ++k) {
+          m[nt][k] -= (float)low;
+          l[nt][k] *= up;
+        }
+        if (down != 1.0f)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[nt][i][j] *= down;
-      ref = vs;
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[nt][i][j] *= down;
+      }
+      if (ref != kNoScale) span += low;
+      ref = ve;
     }
-    const float ratio = vs == ref ? 1.0f : vs / ref;
+    const int gap = some ? min(ref - ve, kSpan) : kZeroSpan;
+    span = max(span, gap);
+    const float ratio = some ? vs * tc::pow2i(-ref) : 0.0f, below = ref == kNoScale ? 0.0f : -(float)gap;
     uint32_t whi[NT][2], wlo[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -335,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         for (int j = 0; j < 4; ++j)
           if (tok + g + 8 * (j >> 1) >= limit[nt][j & 1]) x[j] = -INFINITY;
       }
-      const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
+      const float top0 = fmaxf(x[0], x[2]) + below, top1 = fmaxf(x[1], x[3]) + below;
       const bool move = top0 > m[nt][0] + (kTau + kShift) || top1 > m[nt][1] + (kTau + kShift);
       if (__any_sync(0xffffffffu, move)) {
         float top[2] = {top0, top1};
@@ -363,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
         const float mm = m[nt][j & 1] == -INFINITY ? 0.0f : m[nt][j & 1];
         p[j] = tc::ex2(x[j] - mm);
         l[nt][j & 1] += p[j];
+        p[j] *= ratio;
       }
       uint32_t h0, l0, h1, l1;
       split2(p[0], p[1], h0, l0);
@@ -392,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
           mma(o, f, wlo[nt][0], wlo[nt][1]);
           mma(o, f, whi[nt][0], whi[nt][1]);
           float(&sum)[4] = acc[nt][2 * w + h];
-          const float2 s0 = fma2(make_float2(o[0], o[1]), make_float2(ratio, ratio), make_float2(sum[0], sum[1]));
-          const float2 s1 = fma2(make_float2(o[2], o[3]), make_float2(ratio, ratio), make_float2(sum[2], sum[3]));
+          const float2 s0 = add2(make_float2(sum[0], sum[1]), make_float2(o[0], o[1]));
+          const float2 s1 = add2(make_float2(sum[2], sum[3]), make_float2(o[2], o[3]));
           sum[0] = s0.x, sum[1] = s0.y, sum[2] = s1.x, sum[3] = s1.y;
         }
       }
@@ -404,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge starts and waits for this grid
 
   // -- join the warps: sums over the lanes of a row, then over the warps
+  const float unit = ref == kNoScale ? 0.0f : tc::pow2i(ref);
   float down[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -426,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, resident(D, NT)) split_kernel(Q8Atte
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int byte = 2 * i + (j >> 1);  // byte of this lane's part of a V row
-        sm.acc[warp][2 * t + (j & 1)][v_offset<D>(byte >> 2, g) + (byte & 3)] = acc[nt][i][j] * down[nt][j & 1] * ref;
+        sm.acc[warp][2 * t + (j & 1)][v_offset<D>(byte >> 2, g) + (byte & 3)] = acc[nt][i][j] * down[nt][j & 1] * unit;
       }
     __syncthreads();
     for (int p = threadIdx.x; p < 8 * (D / 4); p += kThreads) {

@@ -272,3 +272,35 @@ def test_long_sums_of_positive_values_keep_their_last_bits():
                     for x, s in ((c.k_codes, c.k_scales), (c.v_codes, c.v_scales)))
             want = torch.softmax(q[b, 2 * h:2 * h + 2].double() @ k.T / 16, -1) @ v
             assert ((got[b, 2 * h:2 * h + 2] / want - 1).abs().max() < 2.0 ** -18)
+
+
+@pytest.mark.parametrize("place", [0, 5, 24])
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_fp32_tokens_of_small_weight_and_huge_value_keep_their_precision(d, n, place):
+    """One block of 16 tokens whose keys score 14 nats below the others' (weights of 1e-6) and whose V is
+    1e5 to 1e20 times theirs, so that it is most of the output or all: at the beginning, between others,
+    at the end.  Blocks of zeros, which score as the others do, around it in every second head.
+    Tolerances of the fp32 rows behind a huge block."""
+    require_cuda()
+    B, H, T = 12, 32, 400
+    g = torch.Generator("cuda").manual_seed(101)
+    c = BlockKVCache(B, H, d, T, block=16)
+    k, v = (torch.randn(B, H, T, d, generator=g, device="cuda") for _ in range(2))
+    k[..., 0] = 0
+    k[:, :, 16 * place:16 * place + 16, 0] = -1
+    size = torch.tensor([1e5, 1e7, 1e10, 1e20], device="cuda").repeat(3)[:, None, None, None]
+    v[:, :, 16 * place:16 * place + 16] *= size
+    v[:, ::2, 32:64] = v[:, ::2, 320:352] = 0
+    if place:
+        v[:, ::2, :16] = 0
+    c.append(k, v, i32([0] * B))
+    q = torch.randn(B, 2 * H, n, d, generator=g, device="cuda")
+    scale = d ** -0.5
+    q[..., 0] = 14 / scale
+    want, weighted, *_ = definition(c, q, T, scale)
+    got = (c.attend(q, i32([T] * B), T) if n > 1 else c.decode(q[:, :, 0].contiguous(), i32([T] * B), T)[:, :, None])
+    kk = c.read(None, T, dtype=F32)[0].abs().double().repeat_interleave(2, 1)
+    spread = scale * (q.abs().double() @ kk.transpose(-1, -2)).amax(-1, keepdim=True)
+    off = ~((got.double() - want).abs() <= 2 * 2.0 ** -20 * (spread + 1) * weighted)
+    assert not off.any(), off.sum((1, 2, 3)).tolist()
