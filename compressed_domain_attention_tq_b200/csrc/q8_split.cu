@@ -30,9 +30,10 @@
 // E grows m falls with it, and O stays as it is.  Sums of weights and O are fp32.
 //
 // Bound: HBM for decode (one pass over the codes).  Measured (int8, bf16 queries, captured
-// calls repeated on one input): d 256, 64K x 4 sequences, 32/16 heads 357 us, 91% of the
-// measured copy rate; d 128, 32K x 8 sequences, 64/8 heads 108 us, 76%; 128K of one
-// sequence 61 us, 67%, about 15 us of it launches, the first step's latency and the merge.  Tiles of 16 rows
+// calls repeated on one input): d 256, 64K x 4 sequences, 32/16 heads 359 us, 91% of the
+// measured copy rate; d 128, 32K x 8 sequences, 64/8 heads 109 us, 75%; 128K of one
+// sequence 62 us, 66% (e4m3 59), about 15 us of it launches, the first step's latency and
+// the merge.  Tiles of 16 rows
 // (NT = 2) convert a code once for two products; they are taken when a kv head
 // has more than 8 rows.
 #include <limits.h>

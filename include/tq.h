@@ -614,8 +614,11 @@ TQ_API size_t tq_sdpa_q8_workspace_bytes(int32_t batch, int32_t num_q_heads, int
  *            position below 0) get zeros; rows of queries i >= q_lens[b] are
  *            left as they were.  fp32 outputs are computed with products split
  *            into two f16 parts (relative error near 1e-6); bf16 outputs of
- *            long query chunks may be computed with weights of 11 bits (an
- *            error well below that of the output's own rounding).
+ *            more than 16 query rows per kv head are computed with weights of
+ *            11 bits (an error well below that of the output's own rounding).
+ *            Both hold as long as the attended blocks' V scales are within a
+ *            factor of 2^90 of one another (and weights, beside blocks of V
+ *            that are all zeros, within 2^45 of those).
  *  lse       NULL, or float [B][Hq][n_q][2], 8-byte aligned: (M, L) with
  *            L = sum_t 2^(attn_scale * q.k_t * log2(e) - M), M between one below
  *            the largest exponent and the logarithm of the sum of all (-inf and
